@@ -7,7 +7,7 @@ pass raw pointers and sizes to the library, and raise ``SQError`` on a
 non-OK status.  Every step of the layer runs in the library's kernels; there
 is no CPU path.  Importing this package on a machine without the built
 library raises ``ImportError`` (build it with
-``python -m w8a8_post_quantization_calib_b200.build``).
+``python w8a8_post_quantization_calib_b200/build.py``).
 
 Names follow the C ABI: ``calib_absmax``, ``smooth_scales``,
 ``quant_weight``, ``smooth_quant_act``, ``linear_w8a8`` (+ ``gemm_s32``,
@@ -63,7 +63,7 @@ class SQError(RuntimeError):
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
-                          "`python -m w8a8_post_quantization_calib_b200.build`")
+                          "`python w8a8_post_quantization_calib_b200/build.py`")
     L = ctypes.CDLL(LIB_PATH)
     P, I64, I, F, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
     sig = {

@@ -12,7 +12,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SO = os.path.join(HERE, "libsq.so")
 SOURCES = ["libsq.cu"]
-HEADERS = ["common.cuh", "ptx_sm100.cuh", "calib.cuh", "quant.cuh", "gemm.cuh"]
+HEADERS = ["common.cuh", "ptx_sm100.cuh", "calib.cuh", "robust.cuh", "quant.cuh", "gemm.cuh"]
 PEAK_SO = os.path.join(HERE, "libsq_peak.so")
 PEAK_SOURCES = ["peak.cu"]
 PEAK_HEADERS = ["common.cuh", "ptx_sm100.cuh"]

@@ -31,7 +31,7 @@ def lib() -> ctypes.CDLL:
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"{LIB_PATH} is missing: build it with "
-                              "`python -m w8a8_post_quantization_calib_b200.build`")
+                              "`python w8a8_post_quantization_calib_b200/build.py`")
         L = ctypes.CDLL(LIB_PATH)
         L.sqpeak_clusters.restype = ctypes.c_int
         L.sqpeak_clusters.argtypes = [ctypes.c_int]
