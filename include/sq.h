@@ -101,7 +101,8 @@ void sq_debug_inject(int what);
 
 /* Synchronises `stream`, then returns SQ_ERR_TIMEOUT if any kernel of this
  * library recorded a barrier timeout on the current device since the last
- * check (and clears the record), SQ_ERR_CUDA if the stream reported an error,
+ * check (and clears the record), SQ_ERR_INVALID_ARG if a kernel of the
+ * key/value cache met an index outside the cache, SQ_ERR_CUDA if the stream reported an error,
  * else SQ_OK. */
 sq_status sq_sync_status(sq_stream stream);
 
@@ -484,6 +485,124 @@ sq_status sq_alpha_search(const void *x_held, const void *w, int64_t M_held, int
                           const float *act_max, const float *w_max, const float *alphas,
                           int n_alpha, void *workspace, size_t workspace_bytes,
                           float *best_alpha, double *mse, sq_stream stream);
+
+/* -------------------------------------------------------------------------
+ * 4-bit microscaled floating point: the same smoothing with E2M1 codes
+ * (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6) that share a scale in blocks along K.
+ *
+ *   SQ_MXFP4  blocks of 32, E8M0 scale 2^(byte - 127)  (OCP Microscaling Formats v1.0)
+ *   SQ_NVFP4  blocks of 16, E4M3 scale, and one fp32 scale g for the tensor
+ *
+ * Canonical fp32 order, with recip(v) = min(fl(1/v), FLT_MAX) for v > 0, else 0:
+ *
+ *   x'    = fl(x * recip(s_j)) (activations) or fl(w * s_j) (weights); s = NULL: x' = x
+ *   m     = max |x'| over the block (columns behind K count as 0)
+ *   MXFP4   byte = max(exponent field of m - 2, 0)       (2^(floor(log2 m) - 2), at least 2^-127)
+ *           code = e2m1(x' * 2^(127 - byte))             value = e2m1 * 2^(byte - 127)
+ *   NVFP4   v = e4m3(fl(m * fl(recip(g) * fl(1/6))))     (saturating at 448)
+ *           code = e2m1(fl(x' * recip(fl(v * g))))       value = fl(e2m1 * fl(v * g))
+ *
+ * e2m1 rounds to nearest, ties to even, and saturates at 6.  A block that
+ * holds an infinity or a NaN gets the NaN scale (0xff, 0x7f): its values, and
+ * every product that reads it, are NaN.
+ *
+ * Codes: two a byte, the even column in the low nibble; a row takes
+ * sq_fp4_code_bytes(K) = 16 * ceil(K / 32) bytes, the codes behind K are 0.
+ * Scales: sq_fp4_scale_bytes(fmt, rows, K) bytes in tiles of 128 rows x 4
+ * blocks (512 bytes), the tiles of 128 rows together; in a tile, the four
+ * bytes of row r lie at 16 * (r % 32) + 4 * (r / 32).  Bytes of blocks behind
+ * K are written as 0, those of rows behind the last are not written.  Codes and scales
+ * 16-byte aligned.
+ * ------------------------------------------------------------------------- */
+typedef enum { SQ_MXFP4 = 0, SQ_NVFP4 = 1 } sq_fp4_format;
+
+size_t sq_fp4_code_bytes(int64_t K);
+size_t sq_fp4_scale_bytes(sq_fp4_format fmt, int64_t rows, int64_t K);
+
+/* sq_smooth_scales with the two tensor scales of NVFP4:
+ *   g_act[0] = fl(max_j fl(act_max_j * recip(s_j)) / 2688)
+ *   g_w[0]   = fl(max_j fl(w_max_j * s_j) / 2688)          (2688 = 6 * 448)
+ * each fp32 [1] or NULL.  s as in sq_smooth_scales. */
+sq_status sq_smooth_scales_nvfp4(const float *act_max, const float *w_max, int64_t K, float alpha, float *s,
+                                 float *g_act, float *g_w, sq_stream stream);
+
+/* Weight w [N, K] of `dt`, contiguous.  s: fp32 [K] or NULL.  g: fp32 [1] or
+ * NULL (1), read for NVFP4 only. */
+sq_status sq_quant_weight_fp4(const void *w, sq_dtype dt, int64_t N, int64_t K, const float *s, sq_fp4_format fmt,
+                              const float *g, uint8_t *wq4, uint8_t *w_sf, sq_stream stream);
+
+/* Activations x [M, K] of `dt`, rows ld >= K elements apart.  M = 0: no-op. */
+sq_status sq_smooth_quant_act_fp4(const void *x, sq_dtype dt, int64_t M, int64_t K, int64_t ld, const float *s,
+                                  sq_fp4_format fmt, const float *g, uint8_t *xq4, uint8_t *x_sf, sq_stream stream);
+
+/* out [rows, K] = RN_out of the codes' values (the smoothing stays in them). */
+sq_status sq_dequant_fp4(const uint8_t *q4, const uint8_t *sf, sq_fp4_format fmt, int64_t rows, int64_t K,
+                         const float *g, sq_dtype out_dt, void *out, sq_stream stream);
+
+/* The product of packed operands of one format:
+ *
+ *   acc[m,n] = sum_k xv[m,k] * wv[n,k]   with xv, wv = e2m1 * block scale (without g), in fp32 on the
+ *              tensor cores (tcgen05 kind::mxf4 / mxf4nvf4; every product is
+ *              exact, the sum is rounded in an unspecified order)
+ *   y[m,n]   = RN_out(fmaf(acc, fl(g_act * g_w), bias[n]))     (a product without bias)
+ *
+ * g_act, g_w: fp32 [1] or NULL (1), read for NVFP4 only.  bias: [N] of out_dt
+ * or NULL.  y: [M, N] of out_dt, contiguous, any N >= 1 (rows of a multiple
+ * of 16 bytes at a 16-byte aligned y take the fast stores).  M = 0: no-op.
+ * No workspace: M <= 128 streams the weight, a cluster of CTAs sharing a
+ * tile's K range where the tiles are few; M > 128 runs CTA pairs. */
+sq_status sq_linear_fp4(const uint8_t *xq4, const uint8_t *x_sf, const uint8_t *wq4, const uint8_t *w_sf,
+                        sq_fp4_format fmt, int64_t M, int64_t N, int64_t K, const float *g_act, const float *g_w,
+                        const void *bias, sq_dtype out_dt, void *y, sq_stream stream);
+
+/* -------------------------------------------------------------------------
+ * Key/value cache in 8 or 4 bits.  The keys and values that a quantised
+ * layer's projections give are quantised as they are written into a paged
+ * cache, one scale a token and head (MXFP4: one a block of 32 along the
+ * head), and widened again as contexts are read back:
+ *
+ *   SQ_KV_INT8   a = fl(max |x| / 127), code = q(fl(x * recip(a))),    value = fl(code * a)
+ *   SQ_KV_FP8    a = fl(max |x| / 448), code = e4m3(fl(x * recip(a))), value = fl(e4m3 * a)
+ *   SQ_KV_MXFP4  as above, without s
+ *
+ * recip as for the 4-bit formats.  A row (INT8, FP8) or block (MXFP4) that
+ * holds an infinity or a NaN reads back as NaN.
+ *
+ * A cache has num_pages pages of page_size tokens; slot = page * page_size +
+ * position in the page.  k_cache, v_cache: [slots, H, sq_kv_row_bytes(fmt, D)]
+ * bytes (the codes behind D are 0); k_scale, v_scale: [slots, H,
+ * sq_kv_scale_bytes(fmt, D)] bytes (one fp32, or ceil(D / 32) E8M0 bytes).
+ * All four 16-byte aligned.  1 <= D <= 1024, else SQ_ERR_UNSUPPORTED.
+ *
+ * Indices are checked on the device: a slot or page outside the cache is not
+ * accessed, and sq_sync_status then returns SQ_ERR_INVALID_ARG (once).
+ * ------------------------------------------------------------------------- */
+typedef enum { SQ_KV_INT8 = 0, SQ_KV_FP8 = 1, SQ_KV_MXFP4 = 2 } sq_kv_format;
+
+size_t sq_kv_row_bytes(sq_kv_format fmt, int64_t D);
+size_t sq_kv_scale_bytes(sq_kv_format fmt, int64_t D);
+
+/* Writes T tokens.  k, v: [T, H, D] of `dt`, tokens k_ld / v_ld >= H * D
+ * elements apart (slices of a fused projection's output).  slots: int64 [T];
+ * a negative slot is skipped (padding).  Slots of one call are distinct: of
+ * two tokens with the same slot, which one's codes and which one's scale stay
+ * is unspecified (other slots are not affected). */
+sq_status sq_kv_cache_write(const void *k, const void *v, sq_dtype dt, int64_t T, int64_t H, int64_t D, int64_t k_ld,
+                            int64_t v_ld, const int64_t *slots, sq_kv_format fmt, int64_t num_slots, void *k_cache,
+                            void *k_scale, void *v_cache, void *v_scale, sq_stream stream);
+
+/* Reads B ragged spans of sequences back.  Sequence b's rows are output rows
+ * cu_rows[b] .. cu_rows[b + 1] - 1 (int32 [B + 1], ascending) and hold its
+ * positions starts[b], starts[b] + 1, ... (int32 [B], or NULL for 0); position
+ * p lies in page table[b, p / page_size] (int32 [B, max_pages]).  k_out,
+ * v_out: [total, H, D] of out_dt, contiguous; rows at cu_rows[B] and behind,
+ * up to total, are left as they were, as are rows before cu_rows[0].  A
+ * position whose page is outside the table or the cache gives zeros. */
+sq_status sq_kv_cache_read(sq_kv_format fmt, const void *k_cache, const void *k_scale, const void *v_cache,
+                           const void *v_scale, int64_t num_pages, int64_t page_size, int64_t H, int64_t D,
+                           const int32_t *table, int64_t B, int64_t max_pages, const int32_t *cu_rows,
+                           const int32_t *starts, int64_t total, sq_dtype out_dt, void *k_out, void *v_out,
+                           sq_stream stream);
 
 #ifdef __cplusplus
 }

@@ -383,6 +383,148 @@ def gemm_fp8_f64(xq: np.ndarray, wq: np.ndarray) -> np.ndarray:
     return e4m3_decode(xq).astype(np.float64) @ e4m3_decode(wq).astype(np.float64).T
 
 
+# ---------------------------------------------------------------- 4-bit microscaled formats
+MXFP4, NVFP4 = 0, 1
+E2M1_POS = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])     # values of codes 0..7, ascending
+_FMAX = np.finfo(np.float32).max
+
+
+def fp4_block(fmt: int) -> int:
+    return 32 if fmt == MXFP4 else 16
+
+
+def e2m1_decode(codes: np.ndarray) -> np.ndarray:
+    """E2M1 codes (0..15, the sign in bit 3) -> fp64 values."""
+    c = np.asarray(codes).astype(np.int64)
+    return np.where(c & 8, -1.0, 1.0) * E2M1_POS[c & 7]
+
+
+def e2m1_encode(v: np.ndarray) -> np.ndarray:
+    """fp32 -> E2M1 codes: nearest value, ties to the even code, beyond 6 saturated.  No NaN."""
+    v = np.asarray(v, np.float32)
+    a = np.abs(v).astype(np.float64)
+    hi = np.clip(np.searchsorted(E2M1_POS, a, side="left"), 0, 7)
+    lo = np.clip(hi - 1, 0, 7)
+    up = (E2M1_POS[hi] - a < a - E2M1_POS[lo]) | ((E2M1_POS[hi] - a == a - E2M1_POS[lo]) & (hi % 2 == 0))
+    code = np.where(a >= 6.0, 7, np.where(up, hi, lo))
+    return (code | np.where(np.signbit(v), 8, 0)).astype(np.uint8)
+
+
+def recip_finite32(v: np.ndarray) -> np.ndarray:
+    """min(fl(1/v), the largest finite number) for v > 0, else 0 (also for NaN)."""
+    v = np.asarray(v, np.float32)
+    with np.errstate(divide="ignore", over="ignore", invalid="ignore"):
+        r = np.minimum(np.float32(1.0) / v, _FMAX)
+    return np.where(v > 0, r, np.float32(0)).astype(np.float32)
+
+
+def e8m0_decode(b: np.ndarray) -> np.ndarray:
+    b = np.asarray(b).astype(np.float64)
+    return np.where(b == 255, np.nan, np.exp2(np.minimum(b, 254) - 127.0))
+
+
+def quant_fp4(x: np.ndarray, fmt: int, s=None, weight: bool = False, g=None, dt: int | None = None):
+    """Blocks of E2M1 codes along the last axis of a 2-D x: (codes [rows, K'], scale bytes [rows, K' / block]) with
+    K' = 32 * ceil(K / 32), zeros behind K.  The order of the fp32 steps is that of the C ABI's canonical order.  A
+    block with an infinity or a NaN has the NaN scale (its codes here are 0, and are not specified)."""
+    x = to_f32(x, F32 if dt is None else dt).astype(np.float32)
+    if s is not None:
+        c = np.asarray(s, np.float32) if weight else recip_finite32(s)
+        with np.errstate(over="ignore", invalid="ignore"):
+            x = (x * c[None, :]).astype(np.float32)
+    rows, K = x.shape
+    Kp, B = -(-K // 32) * 32, fp4_block(fmt)
+    b = np.zeros((rows, Kp), np.float32)
+    b[:, :K] = x
+    b = b.reshape(rows, Kp // B, B)
+    bad = ~np.isfinite(b).all(axis=2)
+    b = np.where(bad[..., None], np.float32(0), b)
+    m = np.abs(b).max(axis=2)
+    if fmt == MXFP4:
+        sf = np.maximum((m.view(np.uint32) >> 23).astype(np.int64) - 2, 0)
+        v = (b * np.exp2(127.0 - sf)[..., None]).astype(np.float32)     # exact, or below the least code
+        sf = np.where(bad, 255, sf)
+    else:
+        g32 = np.float32(1.0) if g is None else np.asarray(g, np.float32).reshape(-1)[0]
+        gc = np.float32(recip_finite32(g32) * np.float32(np.float32(1) / np.float32(6)))
+        with np.errstate(over="ignore"):
+            sf = e4m3_encode((m * gc).astype(np.float32))
+            inv = recip_finite32((e4m3_decode(sf) * g32).astype(np.float32))
+            v = (b * inv[..., None]).astype(np.float32)
+        sf = np.where(bad, 0x7F, sf)
+    return e2m1_encode(v).reshape(rows, Kp), sf.astype(np.uint8)
+
+
+def fp4_values(codes: np.ndarray, sf: np.ndarray, fmt: int, g=None, f32: bool = True) -> np.ndarray:
+    """Values of codes [rows, K'] with scale bytes [rows, K' / block]; f32: fl(code * fl(scale * g)) as dequantised,
+    else the exact fp64 code * scale without g (the product's operands)."""
+    with np.errstate(over="ignore"):
+        if fmt == MXFP4:
+            sc = e8m0_decode(sf)
+        else:
+            sc = e4m3_decode(sf).astype(np.float64)
+            if f32:
+                sc = (sc.astype(np.float32) * (np.float32(1) if g is None else np.asarray(g, np.float32).reshape(-1)[0])
+                      ).astype(np.float64)
+        v = e2m1_decode(codes) * np.repeat(sc, fp4_block(fmt), axis=1)
+        return v.astype(np.float32) if f32 else v
+
+
+def fp4_pack(codes: np.ndarray) -> np.ndarray:
+    """Two codes a byte, the even column in the low nibble."""
+    return (codes[:, 0::2] | (codes[:, 1::2] << 4)).astype(np.uint8)
+
+
+def fp4_unpack(q: np.ndarray) -> np.ndarray:
+    return np.stack([q & 15, q >> 4], axis=-1).reshape(q.shape[0], -1)
+
+
+def fp4_scale_index(rows: int, nblk: int) -> np.ndarray:
+    """Byte of row r's block b in the tiled layout: tiles of 128 rows x 4 blocks, 512 bytes each."""
+    r, b = np.arange(rows)[:, None], np.arange(nblk)[None, :]
+    kt = -(-nblk // 4)
+    return ((r // 128) * kt + b // 4) * 512 + (r % 32) * 16 + (r % 128) // 32 * 4 + b % 4
+
+
+def fp4_scale_size(rows: int, nblk: int) -> int:
+    return -(-rows // 128) * -(-nblk // 4) * 512
+
+
+def fp4_tile_scales(sf: np.ndarray, fill: int = 0) -> np.ndarray:
+    """Scale bytes [rows, blocks] in the tiled layout; rows behind the last hold `fill`, blocks behind the last 0."""
+    rows, n = sf.shape
+    t = np.full(fp4_scale_size(rows, n), fill, np.uint8)
+    t[fp4_scale_index(rows, -(-n // 4) * 4)] = 0
+    t[fp4_scale_index(rows, n)] = sf
+    return t
+
+
+# ---------------------------------------------------------------- key/value cache
+KV_INT8, KV_FP8, KV_MXFP4 = 0, 1, 2
+
+
+def kv_quant(x: np.ndarray, fmt: int, dt: int | None = None):
+    """Rows [n, D] -> (codes [n, D] or packed bytes, scales): the cache's rows without their padding.  Finite x."""
+    x = to_f32(x, F32 if dt is None else dt).astype(np.float32)
+    if fmt == KV_MXFP4:
+        codes, sf = quant_fp4(x, MXFP4)
+        return fp4_pack(codes), sf
+    m = np.abs(x).max(axis=1)
+    a = (m / np.float32(127 if fmt == KV_INT8 else 448)).astype(np.float32)
+    v = (x * recip_finite32(a)[:, None]).astype(np.float32)
+    if fmt == KV_INT8:
+        return np.clip(np.rint(v), -127, 127).astype(np.int8), a
+    return e4m3_encode(v), a
+
+
+def kv_values(codes: np.ndarray, scale: np.ndarray, fmt: int, D: int) -> np.ndarray:
+    """fp32 values [n, D] of cache rows."""
+    if fmt == KV_MXFP4:
+        return fp4_values(fp4_unpack(codes), scale, MXFP4)[:, :D]
+    v = codes.astype(np.float32) if fmt == KV_INT8 else e4m3_decode(codes)
+    return (v[:, :D] * scale[:, None].astype(np.float32)).astype(np.float32)
+
+
 def gemm_s32(xq: np.ndarray, wq: np.ndarray) -> np.ndarray:
     """a6 -- acc = xq . wq^T in exact int32."""
     xq = np.ascontiguousarray(xq, np.int8)

@@ -11,8 +11,12 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SO = os.path.join(HERE, "libsq.so")
-SOURCES = ["libsq.cu"]
-HEADERS = ["common.cuh", "ptx_sm100.cuh", "calib.cuh", "robust.cuh", "quant.cuh", "gemm.cuh"]
+# translation units of libsq.so and the headers each includes
+UNITS = {
+    "libsq.cu": ["common.cuh", "host.cuh", "ptx_sm100.cuh", "calib.cuh", "robust.cuh", "quant.cuh", "gemm.cuh"],
+    "libsq_fp4.cu": ["common.cuh", "host.cuh", "ptx_sm100.cuh", "gemm.cuh", "fp4.cuh", "gemm_fp4.cuh", "kvcache.cuh"],
+}
+OBJ = os.path.join(HERE, "_build")
 PEAK_SO = os.path.join(HERE, "libsq_peak.so")
 PEAK_SOURCES = ["peak.cu"]
 PEAK_HEADERS = ["common.cuh", "ptx_sm100.cuh"]
@@ -20,7 +24,7 @@ PEAK_HEADERS = ["common.cuh", "ptx_sm100.cuh"]
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
     "-gencode", "arch=compute_100a,code=sm_100a",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
     "--expt-relaxed-constexpr",
 ]
 
@@ -40,21 +44,46 @@ def _stale(so: str, sources, headers) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _compile(so: str, sources, verbose: bool, extra) -> None:
-    tmp = so + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, *(extra or []), "-I", os.path.join(ROOT, "include"), "-I", CSRC,
-           "-o", tmp, *[os.path.join(CSRC, f) for f in sources]]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, so)
+def _nvcc_cmd(out: str, args, extra) -> list[str]:
+    return [nvcc(), *NVCC_FLAGS, *(extra or []), "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-o", out, *args]
+
+
+def _run(jobs, verbose: bool) -> None:
+    """Runs compilers side by side.  A job is (temporary, final, command): what a command has made takes its final
+    name; the first failure is raised after all have ended."""
+    procs = []
+    for _, _, cmd in jobs:
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        procs.append(subprocess.Popen(cmd))
+    failed = None
+    for (tmp, final, cmd), p in zip(jobs, procs):
+        if p.wait() == 0:
+            os.replace(tmp, final)
+        else:
+            failed = failed or subprocess.CalledProcessError(p.returncode, cmd)
+    if failed:
+        raise failed
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    if force or _stale(SO, SOURCES, HEADERS):
-        _compile(SO, SOURCES, verbose, extra)
+    os.makedirs(OBJ, exist_ok=True)
+    tag = f".tmp{os.getpid()}"
+
+    def job(final, args, flags=extra):
+        return final + tag, final, _nvcc_cmd(final + tag, args, flags)
+
+    jobs = []
+    for unit, headers in UNITS.items():
+        obj = os.path.join(OBJ, unit[:-3] + ".o")
+        if force or _stale(obj, [unit], headers):
+            jobs.append(job(obj, ["-c", os.path.join(CSRC, unit)]))
     if force or _stale(PEAK_SO, PEAK_SOURCES, PEAK_HEADERS):
-        _compile(PEAK_SO, PEAK_SOURCES, verbose, extra)
+        jobs.append(job(PEAK_SO, ["-shared", *[os.path.join(CSRC, f) for f in PEAK_SOURCES]]))
+    _run(jobs, verbose)
+    objs = [os.path.join(OBJ, unit[:-3] + ".o") for unit in UNITS]
+    if force or not os.path.exists(SO) or any(os.path.getmtime(o) > os.path.getmtime(SO) for o in objs):
+        _run([job(SO, ["-shared", *objs], None)], verbose)
     return SO
 
 

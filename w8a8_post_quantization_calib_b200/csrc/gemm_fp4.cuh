@@ -1,0 +1,647 @@
+// gemm_fp4.cuh -- the product of 4-bit microscaled operands on the block-scaled
+// tensor cores of sm_100a:
+//
+//   acc[m, n] = sum_b sx[m, b] * sw[n, b] * sum_{k in b} x[m, k] * w[n, k]     (b: blocks along K)
+//   y[m, n]   = RN_out(fmaf(acc, fl(g_act * g_w), bias[n]))
+//
+// tcgen05.mma kind::mxf4 (E8M0 scales, blocks of 32) or kind::mxf4nvf4 (E4M3
+// scales, blocks of 16): 64 elements of K an instruction, packed two a byte,
+// so an operand tile is the same 128-byte-swizzled K-major tile as for the
+// 8-bit kernels with twice the elements.  The scales are read from tensor
+// memory: a scale tile (128 rows x 4 blocks, 512 bytes, laid out as in
+// fp4.cuh) comes into shared memory by TMA with its operand's K block, and
+// tcgen05.cp copies it to 4 TMEM columns (row r at lane r % 32, column r / 32,
+// replicated to the four lane quarters).  The copy and the MMAs that read it
+// are issued by one thread and execute in order, so the columns need no
+// barrier.
+//
+// Roles, barriers and the two orientations are those of gemm.cuh:
+//   k_fp4_swap (M <= 128): the weights fill the 128-row MMA and stream once;
+//     a cluster of CS CTAs shares a tile's K range where tiles are few.
+//   k_fp4_pair (M > 128): CTA pairs (cta_group::2), 256 x BN tiles.  Each CTA
+//     loads its 128 rows of A and BN/2 rows of B, its rows' A scales and all
+//     BN rows' B scales (each SM scales its own 128 x BN accumulator).
+#pragma once
+
+#include "fp4.cuh"
+#include "gemm.cuh"
+
+namespace sq {
+namespace fp4 {
+
+using gemm::BKB;
+using gemm::BM;
+using gemm::ERR_DRAIN;
+using gemm::ERR_EPI;
+using gemm::ERR_MMA;
+using gemm::ERR_PRODUCER;
+using gemm::NUM_THREADS;
+using gemm::Params;
+using gemm::STG_BYTES;
+
+// Scale tiles of a 128-byte K block (256 elements), and MMAs that share one.
+template <int FMT> struct SfT {
+    static constexpr int TILES = 256 / FmtT<FMT>::TILE_K;          // MXFP4 2, NVFP4 4
+    static constexpr int MMAS = 4 / TILES;
+};
+
+// The two factors besides the block scales, fl(g_act * g_w).
+struct Fp4Params {
+    Params p;
+    const float *g_act, *g_w;      // [1] or null (1)
+    int direct;                    // pair kernel: the output takes plain stores (rows not 16-byte strided)
+};
+
+// Instruction descriptor of kind::mxf4 / mxf4nvf4, dense, K-major, E2M1 x E2M1
+// -> f32: B scale id at bit 4, the element formats (1: E2M1) at 7 and 10,
+// N / 8 at 17, the scale format (1: E8M0, 0: E4M3) at 23, M / 128 at 27, A
+// scale id at 29.  A scale id is the byte of a TMEM word at which this
+// instruction's scales start.
+template <int FMT>
+__host__ __device__ constexpr uint32_t idesc_fp4(int m, int n, int id)
+{
+    return (static_cast<uint32_t>(id) << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+           ((FMT == FMT_MX ? 1u : 0u) << 23) | (static_cast<uint32_t>(m >> 7) << 27) |
+           (static_cast<uint32_t>(id) << 29);
+}
+
+// Shared-memory descriptor of one scale tile: 32 rows of 16 bytes without
+// swizzle, 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr)
+{
+    return static_cast<uint64_t>((saddr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 16) |
+           (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
+template <int CG>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr)
+{
+    const uint64_t d = sdesc_scales(saddr);
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+template <int FMT, int CG>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, uint32_t accumulate)
+{
+#define SQ_MMA_FP4(CGS, KINDS)                                                                         \
+    asm volatile("{\n\t.reg .pred p;\n\t"                                                              \
+                 "setp.ne.b32 p, %4, 0;\n\t"                                                           \
+                 "tcgen05.mma.cta_group::" CGS "." KINDS " [%0], %1, %2, %3, [%5], [%6], p;\n\t}\n" ::"r"(d), \
+                 "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)                      \
+                 : "memory")
+    if constexpr (FMT == FMT_MX && CG == 1) SQ_MMA_FP4("1", "kind::mxf4.block_scale.scale_vec::2X");
+    else if constexpr (FMT == FMT_MX) SQ_MMA_FP4("2", "kind::mxf4.block_scale.scale_vec::2X");
+    else if constexpr (CG == 1) SQ_MMA_FP4("1", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+    else SQ_MMA_FP4("2", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+#undef SQ_MMA_FP4
+}
+
+// fl(g_act * g_w), absent factors 1
+__device__ __forceinline__ float out_factor(const Fp4Params &fp)
+{
+    return __fmul_rn(fp.g_act != nullptr ? __ldg(fp.g_act) : 1.0f, fp.g_w != nullptr ? __ldg(fp.g_w) : 1.0f);
+}
+
+// ---------------------------------------------------------------------------
+// Small M: A = weights [N, K], B = activations [M, K] (M <= 128, one token
+// tile), one weight tile per cluster of CS CTAs.
+// ---------------------------------------------------------------------------
+template <int BN, int KBO, int FMT>
+struct SwapCfg {
+    using Sf = SfT<FMT>;
+    static constexpr int A_KB = BM * BKB, B_KB = BN * BKB;
+    static constexpr int A_BYTES = A_KB * KBO, B_BYTES = B_KB * KBO;
+    static constexpr int SF_BYTES = KBO * Sf::TILES * SF_TILE;     // of one operand's 128 rows
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 2 * SF_BYTES;
+    static constexpr int STAGES_RAW = 220 * 1024 / STAGE_BYTES;
+    static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
+    static constexpr int SF_COLS = KBO * Sf::TILES * 4;
+    static constexpr int TMEM_COLS = gemm::pow2_at_least(BN + 2 * SF_COLS, 32);
+    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 512;
+    static_assert(STAGE_BYTES % 1024 == 0, "stage must keep 1024-byte alignment");
+    static_assert((2 * STAGES + 4) * 8 + 16 <= 512, "barrier area");
+    static_assert(TMEM_COLS <= 512, "accumulator and scales must fit TMEM");
+};
+
+template <int BN, int KBO, int CS, int FMT>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    k_fp4_swap(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+               const __grid_constant__ CUtensorMap map_ws, const __grid_constant__ CUtensorMap map_xs,
+               const Fp4Params fp)
+{
+    using C = SwapCfg<BN, KBO, FMT>;
+    using Sf = SfT<FMT>;
+    constexpr int S = C::STAGES;
+    static_assert((CS - 1) * BN * BM * 4 <= S * C::STAGE_BYTES, "partial sums must fit the leader's stages");
+    const Params &p = fp.p;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S * C::STAGE_BYTES);
+    const uint32_t bar0 = ptx::smem_addr(bars);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
+    const uint32_t tfull_bar = bar0 + 8u * (2 * S);
+    const uint32_t done_bar = bar0 + 8u * (2 * S + 1);
+    const uint32_t go_bar = bar0 + 8u * (2 * S + 2);      // cluster split: leader's stages free
+    const uint32_t part_bar = bar0 + 8u * (2 * S + 3);    // cluster split: partial sums arrived
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 4);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *flag = reinterpret_cast<int *>(tmem_slot + 2);
+    __shared__ float s_am[BN];
+    const uint32_t sbase = ptx::smem_addr(smem);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(full_bar(s), 1);
+            ptx::mbar_init(empty_bar(s), 1);
+        }
+        ptx::mbar_init(tfull_bar, 1);
+        ptx::mbar_init(done_bar, 1);
+        if constexpr (CS > 1) {
+            ptx::mbar_init(go_bar, 1);
+            ptx::mbar_init(part_bar, CS - 1);
+        }
+        *abort_flag = 0;
+        *flag = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        ptx::tma_prefetch_desc(&map_w);
+        ptx::tma_prefetch_desc(&map_x);
+        ptx::tma_prefetch_desc(&map_ws);
+        ptx::tma_prefetch_desc(&map_xs);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_addr(tmem_slot), C::TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if constexpr (CS > 1) ptx::cluster_sync();   // every CTA's barriers exist before any remote arrive
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const uint64_t tmo = p.timeout_ns;
+    // this CTA's share of its tile's K groups
+    const int tile = static_cast<int>(blockIdx.x) / CS, part = static_cast<int>(blockIdx.x) % CS;
+    const int kb_begin = static_cast<int>(static_cast<int64_t>(part) * p.num_kb / CS);
+    const int kb_end = static_cast<int>(static_cast<int64_t>(part + 1) * p.num_kb / CS);
+    pdl_wait();                        // operands and scales come from the previous kernels
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            for (int kb = kb_begin; kb < kb_end && !*abort_flag; ++kb) {
+                if (!ptx::wait_bounded(empty_bar(stage), phase ^ 1u, tmo, abort_flag, ERR_PRODUCER)) break;
+                const bool withhold = p.inject == 1 && blockIdx.x == 0 && issued == 0;
+                if (!withhold) {
+                    const uint32_t fb = full_bar(stage);
+                    ptx::mbar_arrive_expect_tx(fb, C::STAGE_BYTES);
+                    const uint32_t sa = sbase + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
+                    const uint32_t ssa = sb + C::B_BYTES, ssb = ssa + C::SF_BYTES;
+                    if constexpr (KBO == 1) {
+                        ptx::tma_load_2d(sa, &map_w, fb, kb * BKB, tile * BM);
+                        ptx::tma_load_2d(sb, &map_x, fb, kb * BKB, 0);
+                    } else {
+                        ptx::tma_load_3d(sa, &map_w, fb, 0, tile * BM, kb * KBO);
+                        ptx::tma_load_3d(sb, &map_x, fb, 0, 0, kb * KBO);
+                    }
+                    ptx::tma_load_3d(ssa, &map_ws, fb, 0, kb * KBO * Sf::TILES, tile);
+                    ptx::tma_load_3d(ssb, &map_xs, fb, 0, kb * KBO * Sf::TILES, 0);
+                }
+                ++issued;
+                if (++stage == S) { stage = 0; phase ^= 1u; }
+            }
+            // drain: every issued load lands before the CTA exits
+            const int n_wait = issued < S ? issued : S;
+            for (int i = 0; i < n_wait; ++i) {
+                int s = stage - 1 - i;
+                uint32_t ph = phase;
+                if (s < 0) { s += S; ph ^= 1u; }
+                volatile int no_abort = 0;
+                ptx::wait_bounded(full_bar(s), ph, tmo, &no_abort, ERR_DRAIN);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            const uint32_t sfa0 = tmem_base + BN, sfb0 = sfa0 + C::SF_COLS;
+            for (int kb = kb_begin; kb < kb_end; ++kb) {
+                if (!ptx::wait_bounded(full_bar(stage), phase, tmo, abort_flag, ERR_MMA + 1)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t sa = sbase + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
+                const uint32_t ssa = sb + C::B_BYTES, ssb = ssa + C::SF_BYTES;
+#pragma unroll
+                for (int i = 0; i < KBO * Sf::TILES; ++i) {
+                    copy_scales<1>(sfa0 + 4 * i, ssa + i * SF_TILE);
+                    copy_scales<1>(sfb0 + 4 * i, ssb + i * SF_TILE);
+                }
+#pragma unroll
+                for (int j = 0; j < KBO; ++j) {
+                    const uint64_t ad = ptx::sdesc_kmajor_sw128(sa + j * C::A_KB);
+                    const uint64_t bd = ptx::sdesc_kmajor_sw128(sb + j * C::B_KB);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int t = j * Sf::TILES + k / Sf::MMAS;
+                        mma_fp4<FMT, 1>(tmem_base, ad + 2 * k, bd + 2 * k,
+                                        idesc_fp4<FMT>(128, BN, (k % Sf::MMAS) * 2), sfa0 + 4 * t, sfb0 + 4 * t,
+                                        (kb > kb_begin || j > 0 || k > 0) ? 1u : 0u);
+                    }
+                }
+                ptx::tc_commit(empty_bar(stage));
+                if (++stage == S) { stage = 0; phase ^= 1u; }
+            }
+            if (ok) ptx::tc_commit(tfull_bar);
+            // drain: all issued MMAs complete before TMEM is released
+            ptx::tc_commit(done_bar);
+            volatile int no_abort = 0;
+            ptx::wait_bounded(done_bar, 0u, tmo, &no_abort, ERR_DRAIN + 1);
+        }
+    } else {
+        // ------------------------------------------------ epilogue (warps 2..5)
+        const int q = warp & 3;
+        for (int m = threadIdx.x - 64; m < BN; m += 128) s_am[m] = 1.0f;
+        const int n = tile * BM + q * 32 + lane;
+        const float factor = out_factor(fp);
+        const float bn = n < p.N ? gemm::load_bias(p.bias, p.out_dt, n) : 0.0f;
+        ptx::named_bar_sync(1, 128);
+        auto tfull_wait = [&]() {
+            int ok = 1;
+            if (lane == 0) ok = ptx::wait_bounded(tfull_bar, 0u, tmo, abort_flag, ERR_EPI) ? 1 : 0;
+            return __shfl_sync(0xffffffffu, ok, 0) != 0;
+        };
+        const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+        if constexpr (CS > 1)
+            gemm::epilogue_cs<BN, gemm::EPI_DEQUANT, CS, gemm::KIND_F8>(p, tbase, tile, 0, q, lane,
+                                                                       ptx::cluster_ctarank(), factor, bn, s_am,
+                                                                       tfull_wait, go_bar, part_bar, sbase, abort_flag);
+        else
+            gemm::epilogue_sk<BN, gemm::EPI_DEQUANT, gemm::KIND_F8>(p, tbase, tile, 0, tile, q, lane, flag, abort_flag,
+                                                                    factor, bn, s_am, tfull_wait);
+        ptx::tc_fence_before();
+    }
+
+    // warps 0 and 1 ran their role on lane 0 alone: reconverge them first
+    __syncwarp();
+    ptx::tc_fence_before();
+    if constexpr (CS > 1) ptx::cluster_sync();   // no CTA leaves while another may still write to its stages
+    else __syncthreads();
+    pdl_trigger();                     // every output of this CTA is written
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem_base, C::TMEM_COLS);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Large M: CTA pairs, 256 x BN tiles.  TMEM holds two accumulators and the
+// scale columns of a stage.  256-wide tiles leave no room for two whole
+// accumulators beside the scales: the second starts ACC_STRIDE < BN columns
+// behind the first and shares OVERLAP columns with it.  The epilogue drains the
+// shared columns first, and the next tile's MMAs start once they are free, so
+// the rest of the epilogue still overlaps them.
+// ---------------------------------------------------------------------------
+template <int BN, int KBO, int FMT>
+struct Pair4Cfg {
+    using Sf = SfT<FMT>;
+    static constexpr int A_KB = BM * BKB, B_KB = (BN / 2) * BKB;
+    static constexpr int A_BYTES = A_KB * KBO, B_BYTES = B_KB * KBO;
+    static constexpr int NB = (BN % 128) == 0 ? BN / 128 : BN / 128 + 1;     // row tiles of B's scales
+    static constexpr int SFA_BYTES = KBO * Sf::TILES * SF_TILE, SFB_BYTES = NB * SFA_BYTES;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
+    static constexpr int STG_BUFS = 1;
+    static constexpr int STG_TOTAL = 4 * STG_BUFS * STG_BYTES;
+    static constexpr int COLS_BYTES = 2 * 256 * 4;          // the tile's bias, two tiles
+    static constexpr int FIXED_BYTES = 1024 + STG_TOTAL + COLS_BYTES + 256;
+    static constexpr int STAGES_RAW = (227 * 1024 - FIXED_BYTES) / STAGE_BYTES;
+    static constexpr int STAGES = STAGES_RAW > 10 ? 10 : STAGES_RAW;
+    static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * STAGE_BYTES;
+    static constexpr int SFA_COLS = KBO * Sf::TILES * 4, SFB_COLS = NB * SFA_COLS;
+    static constexpr int SF_COLS = SFA_COLS + SFB_COLS;
+    static constexpr int ACC_STRIDE = (512 - SF_COLS - BN) / 32 * 32 < BN ? (512 - SF_COLS - BN) / 32 * 32 : BN;
+    static constexpr int OVERLAP = BN - ACC_STRIDE;         // a multiple of 32
+    static constexpr int SF_COL0 = ACC_STRIDE + BN;
+    static constexpr int TMEM_COLS = gemm::pow2_at_least(SF_COL0 + SF_COLS, 32);
+    static_assert(STAGE_BYTES % 1024 == 0, "stage must keep 1024-byte alignment");
+    static_assert(BN % 64 == 0 && BN >= 128 && BN <= 256, "pair MMA N");
+    static_assert(TMEM_COLS <= 512 && ACC_STRIDE > 0, "accumulators and scales must fit TMEM");
+    static_assert((2 * STAGES + 6) * 8 + 16 <= 256, "barrier area");
+};
+
+// One 32-column chunk of an accumulator: factor, bias, rounding, store.
+template <int BN>
+__device__ __forceinline__ void epilogue_chunk(const Fp4Params &fp, const CUtensorMap *omap, const uint32_t (&r)[32],
+                                               int n0, int mrow0, int lane, uint32_t buf, bool first, float factor,
+                                               const float *bias_tile)
+{
+    const Params &p = fp.p;
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        const float4 b4 = *reinterpret_cast<const float4 *>(bias_tile + i);        // broadcast
+        const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+        for (int t = 0; t < 4; ++t) v[i + t] = gemm::dequant(__uint_as_float(r[i + t]), factor, p.bias, bb[t]);
+    }
+    if (fp.direct) {
+        const int m = mrow0 + lane;
+        if (m < p.M) {
+            const int nval = min(32, p.N - n0);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i < nval) gemm::store_out(p.out, p.out_dt, static_cast<int64_t>(m) * p.N + n0 + i, v[i]);
+        }
+        return;
+    }
+    uint32_t w[32];
+    const bool wide = p.out_dt == DT_F32;
+    if (wide) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+    } else if (p.out_dt == DT_F16) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    }
+    // the staging buffer is rewritten only once the store issued from it has
+    // finished reading shared memory
+    if (lane == 0 && !first) ptx::bulk_wait_read_0();
+    __syncwarp();
+    const int pieces = wide ? 8 : 4;           // 128-byte rows, chunk ^= row & 7; or 64-byte rows, chunk ^= (row >> 1) & 3
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if (k < pieces) {
+            const uint32_t a = wide ? buf + lane * 128 + ((k ^ (lane & 7)) << 4)
+                                    : buf + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[4 * k]), "r"(w[4 * k + 1]),
+                         "r"(w[4 * k + 2]), "r"(w[4 * k + 3])
+                         : "memory");
+        }
+    }
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        ptx::tma_store_2d(omap, buf, n0, mrow0);
+        ptx::bulk_commit();
+    }
+}
+
+template <int BN, int KBO, int FMT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+    k_fp4_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+               const __grid_constant__ CUtensorMap map_as, const __grid_constant__ CUtensorMap map_bs,
+               const __grid_constant__ CUtensorMap map_o, const Fp4Params fp)
+{
+    using C = Pair4Cfg<BN, KBO, FMT>;
+    using Sf = SfT<FMT>;
+    constexpr int S = C::STAGES;
+    const Params &p = fp.p;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S * C::STAGE_BYTES + C::STG_TOTAL + C::COLS_BYTES);
+    const uint32_t bar0 = ptx::smem_addr(bars);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
+    auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * S + b); };
+    auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * S + 2 + b); };
+    const uint32_t done_bar = bar0 + 8u * (2 * S + 4);
+    const uint32_t shared_bar = bar0 + 8u * (2 * S + 5);       // the shared accumulator columns are drained
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 6);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *ok_flag = reinterpret_cast<volatile int *>(tmem_slot + 2);     // [2]
+    const uint32_t sbase = ptx::smem_addr(smem);
+    const uint32_t stg_base = sbase + S * C::STAGE_BYTES;
+    float *cols = reinterpret_cast<float *>(smem + S * C::STAGE_BYTES + C::STG_TOTAL);   // [2][256] bias
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const bool leader = (rank == 0);
+    const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(full_bar(s), 1);
+            ptx::mbar_init(empty_bar(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(tfull_bar(b), 1);
+            ptx::mbar_init(tempty_bar(b), 8);
+        }
+        ptx::mbar_init(done_bar, 1);
+        ptx::mbar_init(shared_bar, 8);
+        *abort_flag = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        ptx::tma_prefetch_desc(&map_a);
+        ptx::tma_prefetch_desc(&map_b);
+        ptx::tma_prefetch_desc(&map_as);
+        ptx::tma_prefetch_desc(&map_bs);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(ptx::smem_addr(tmem_slot), C::TMEM_COLS);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    ptx::cluster_sync();               // both CTAs' barriers exist before any remote use
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const uint64_t tmo = p.timeout_ns;
+    pdl_wait();                        // operands and scales come from the previous kernels
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer (both CTAs)
+        if (lane == 0) {
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            for (int u = cluster; u < p.num_units && !*abort_flag; u += nclusters) {
+                int tr, tc;
+                gemm::decode_unit(p, u, tr, tc);
+                bool ok = true;
+                const int ta = 2 * tr + static_cast<int>(rank);              // 128-row tile of A
+                const int yb = tc * BN + static_cast<int>(rank) * (BN / 2);
+                for (int kb = 0; kb < p.num_kb; ++kb) {
+                    if (!ptx::wait_bounded(empty_bar(stage), phase ^ 1u, tmo, abort_flag, ERR_PRODUCER)) {
+                        ok = false;
+                        break;
+                    }
+                    const bool withhold = p.inject == 1 && blockIdx.x == 0 && issued == 0;
+                    if (!withhold) {
+                        if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), 2 * C::STAGE_BYTES);
+                        const uint32_t fb = ptx::map_to_rank(full_bar(stage), 0);
+                        const uint32_t sa = sbase + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
+                        const uint32_t ssa = sb + C::B_BYTES, ssb = ssa + C::SFA_BYTES;
+                        if constexpr (KBO == 1) {
+                            ptx::tma_load_2d_pair(sa, &map_a, fb, kb * BKB, ta * BM);
+                            ptx::tma_load_2d_pair(sb, &map_b, fb, kb * BKB, yb);
+                        } else {
+                            ptx::tma_load_3d_pair(sa, &map_a, fb, 0, ta * BM, kb * KBO);
+                            ptx::tma_load_3d_pair(sb, &map_b, fb, 0, yb, kb * KBO);
+                        }
+                        ptx::tma_load_3d_pair(ssa, &map_as, fb, 0, kb * KBO * Sf::TILES, ta);
+                        ptx::tma_load_3d_pair(ssb, &map_bs, fb, 0, kb * KBO * Sf::TILES, tc * BN / 128);
+                    }
+                    ++issued;
+                    if (++stage == S) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+            }
+            // drain: the leader's full barriers count both CTAs' bytes
+            if (leader) {
+                const int n_wait = issued < S ? issued : S;
+                for (int i = 0; i < n_wait; ++i) {
+                    int s = stage - 1 - i;
+                    uint32_t ph = phase;
+                    if (s < 0) { s += S; ph ^= 1u; }
+                    volatile int no_abort = 0;
+                    ptx::wait_bounded(full_bar(s), ph, tmo, &no_abort, ERR_DRAIN);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer (leader only)
+        if (lane == 0 && leader) {
+            int stage = 0, local = 0;
+            uint32_t phase = 0;
+            const uint32_t sfa0 = tmem_base + C::SF_COL0, sfb0 = sfa0 + C::SFA_COLS;
+            for (int u = cluster; u < p.num_units; u += nclusters, ++local) {
+                const int b = local & 1;
+                const uint32_t use = static_cast<uint32_t>(local >> 1) & 1u;
+                if (!ptx::wait_bounded(tempty_bar(b), use ^ 1u, tmo, abort_flag, ERR_MMA)) break;
+                if (C::OVERLAP > 0 && local > 0 &&
+                    !ptx::wait_bounded(shared_bar, static_cast<uint32_t>(local - 1) & 1u, tmo, abort_flag, ERR_MMA + 2))
+                    break;
+                ptx::tc_fence_after();
+                const uint32_t d = tmem_base + static_cast<uint32_t>(b * C::ACC_STRIDE);
+                int tr, tc;
+                gemm::decode_unit(p, u, tr, tc);
+                // a tile that starts in the middle of a row tile of scales
+                // starts 2 columns (64 rows) into the copy
+                const uint32_t shift = (BN % 128) != 0 ? static_cast<uint32_t>((tc * BN) % 128 / 32) : 0u;
+                bool ok = true;
+                for (int kb = 0; kb < p.num_kb; ++kb) {
+                    if (!ptx::wait_bounded(full_bar(stage), phase, tmo, abort_flag, ERR_MMA + 1)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t sa = sbase + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
+                    const uint32_t ssa = sb + C::B_BYTES, ssb = ssa + C::SFA_BYTES;
+#pragma unroll
+                    for (int i = 0; i < KBO * Sf::TILES; ++i) {
+                        copy_scales<2>(sfa0 + 4 * i, ssa + i * SF_TILE);
+#pragma unroll
+                        for (int t = 0; t < C::NB; ++t)
+                            copy_scales<2>(sfb0 + 4 * (i * C::NB + t), ssb + (t * KBO * Sf::TILES + i) * SF_TILE);
+                    }
+#pragma unroll
+                    for (int j = 0; j < KBO; ++j) {
+                        const uint64_t ad = ptx::sdesc_kmajor_sw128(sa + j * C::A_KB);
+                        const uint64_t bd = ptx::sdesc_kmajor_sw128(sb + j * C::B_KB);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int t = j * Sf::TILES + k / Sf::MMAS;
+                            mma_fp4<FMT, 2>(d, ad + 2 * k, bd + 2 * k, idesc_fp4<FMT>(256, BN, (k % Sf::MMAS) * 2),
+                                            sfa0 + 4 * t, sfb0 + 4 * C::NB * t + shift,
+                                            (kb > 0 || j > 0 || k > 0) ? 1u : 0u);
+                        }
+                    }
+                    ptx::tc_commit_pair_mc(empty_bar(stage), 0x3);
+                    if (++stage == S) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                ptx::tc_commit_pair_mc(tfull_bar(b), 0x3);
+            }
+            ptx::tc_commit_pair(done_bar);
+            volatile int no_abort = 0;
+            ptx::wait_bounded(done_bar, 0u, tmo, &no_abort, ERR_DRAIN + 1);
+        }
+    } else {
+        // ------------------------------------------------ epilogue (warps 2..5, both CTAs)
+        const int q = warp & 3;
+        const uint32_t stg = stg_base + static_cast<uint32_t>((warp - 2) * STG_BYTES);
+        const float factor = out_factor(fp);
+        bool first = true;
+        int local = 0;
+        for (int u = cluster; u < p.num_units; u += nclusters, ++local) {
+            int tr, tc;
+            gemm::decode_unit(p, u, tr, tc);
+            const int b = local & 1;
+            const uint32_t use = static_cast<uint32_t>(local >> 1) & 1u;
+            float *bias_tile = cols + b * 256;
+            for (int t = threadIdx.x - 64; t < BN; t += 128) {
+                const int n = tc * BN + t;
+                bias_tile[t] = n < p.N ? gemm::load_bias(p.bias, p.out_dt, n) : 0.0f;
+            }
+            // one thread waits for the accumulator; the 128 epilogue threads
+            // then take the same decision (no warp is left at a barrier alone)
+            if (threadIdx.x == 64) ok_flag[b] = ptx::wait_bounded(tfull_bar(b), use, tmo, abort_flag, ERR_EPI) ? 1 : 0;
+            ptx::named_bar_sync(1, 128);
+            if (!ok_flag[b]) break;
+            ptx::tc_fence_after();
+            const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                   static_cast<uint32_t>(b * C::ACC_STRIDE);
+            const int mrow0 = (2 * tr + static_cast<int>(rank)) * BM + q * 32;
+            // the columns shared with the other accumulator first: the last
+            // ones of the first accumulator, the first ones of the second
+#pragma unroll 1
+            for (int i = 0; i < BN / 32; ++i) {
+                const int c = (C::OVERLAP > 0 && b == 0) ? BN / 32 - 1 - i : i;
+                uint32_t r[32];
+                ptx::tmem_ld32(tbase + c * 32, r);
+                ptx::tmem_ld_wait();
+                if (C::OVERLAP > 0 && i == C::OVERLAP / 32 - 1) {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(shared_bar, 0));
+                }
+                if (i == BN / 32 - 1) {        // the accumulator is in registers
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(tempty_bar(b), 0));
+                }
+                const int n0 = tc * BN + c * 32;
+                if (n0 >= p.N) continue;
+                epilogue_chunk<BN>(fp, &map_o, r, n0, mrow0, lane, stg, first, factor, bias_tile + c * 32);
+                first = false;
+            }
+        }
+        if (lane == 0) ptx::bulk_wait_all();     // output stores complete before the CTA exits
+        __syncwarp();
+    }
+
+    ptx::tc_fence_before();
+    ptx::cluster_sync();               // no CTA leaves while its peer may still signal it
+    pdl_trigger();                     // every output of this CTA is written (TMA stores waited for)
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    }
+}
+
+}  // namespace fp4
+}  // namespace sq

@@ -1,0 +1,476 @@
+// libsq_fp4.cu -- the C ABI of the 4-bit microscaled formats (quantisation,
+// values, product) and of the quantised key/value cache.  Like libsq.cu:
+// validates arguments, sizes grids, encodes TMA tensor maps and launches; the
+// contract of every entry point is in include/sq.h.
+#include <cstring>
+#include <type_traits>
+
+#include "host.cuh"
+#include "ptx_sm100.cuh"
+#include "fp4.cuh"
+#include "gemm_fp4.cuh"
+#include "kvcache.cuh"
+
+using namespace sq;
+
+namespace sq {
+
+cudaError_t fp4_error_word_take(unsigned int *word)
+{
+    *word = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(word, g_error_word, sizeof(*word));
+    if (e != cudaSuccess || *word == 0) return e;
+    const unsigned int zero = 0;
+    return cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero));
+}
+
+}  // namespace sq
+
+namespace {
+
+inline bool valid_fmt(int f) { return f == SQ_MXFP4 || f == SQ_NVFP4; }
+
+// The widest load (32 or 16 bytes, 0: single elements) that every 16-element
+// piece of rows `ld_bytes` apart allows.
+inline int vec_bytes(const void *p, int64_t ld_bytes)
+{
+    const uint64_t a = reinterpret_cast<uint64_t>(p) | static_cast<uint64_t>(ld_bytes);
+    return (a & 31) == 0 ? 32 : (a & 15) == 0 ? 16 : 0;
+}
+
+// Column strips of 512 x slabs of rows: enough blocks for `per_sm` a SM, a
+// slab no shorter than one pass of the block.
+inline dim3 strip_grid(int64_t rows, int64_t cols, int pass, int per_sm, int64_t &slab)
+{
+    const int64_t gx = cdiv(cols, 16 * fp4::QTX);
+    const int64_t target = std::max<int64_t>(1, cdiv(static_cast<int64_t>(sm_count()) * per_sm, gx));
+    int64_t gy = std::max<int64_t>(1, std::min<int64_t>(cdiv(rows, pass), target));
+    gy = std::min<int64_t>(gy, 65535);
+    slab = cdiv(rows, gy);
+    return dim3(static_cast<unsigned>(gx), static_cast<unsigned>(cdiv(rows, slab)));
+}
+
+template <int DT, int VEC, int FMT>
+cudaError_t launch_quant(fp4::QuantArgs a, cudaStream_t st)
+{
+    const int64_t cols = fp4::scale_tiles_k(FMT, a.K) * fp4::FmtT<FMT>::TILE_K;    // every byte of the scale tiles
+    const dim3 grid = strip_grid(a.rows, cols, fp4::QTY, 8, a.slab);
+    return launch_pdl(fp4::k_fp4_quant<DT, VEC, FMT>, grid, dim3(fp4::QTX, fp4::QTY), 0, st, a);
+}
+
+template <int DT, int VEC>
+cudaError_t launch_quant_fmt(const fp4::QuantArgs &a, int fmt, cudaStream_t st)
+{
+    return fmt == SQ_MXFP4 ? launch_quant<DT, VEC, fp4::FMT_MX>(a, st) : launch_quant<DT, VEC, fp4::FMT_NV>(a, st);
+}
+
+template <int DT>
+cudaError_t launch_quant_vec(const fp4::QuantArgs &a, int fmt, cudaStream_t st)
+{
+    const int vec = vec_bytes(a.x, a.ld * dtype_size(DT));
+    if (vec == 32) return launch_quant_fmt<DT, 32>(a, fmt, st);
+    if (vec == 16) return launch_quant_fmt<DT, 16>(a, fmt, st);
+    return launch_quant_fmt<DT, 0>(a, fmt, st);
+}
+
+sq_status quant_fp4(const void *x, int dt, int64_t rows, int64_t K, int64_t ld, const float *s, int weight, int fmt,
+                    const float *g, uint8_t *q, uint8_t *sf, sq_stream stream)
+{
+    if (x == nullptr || q == nullptr || sf == nullptr || !valid_dt(dt) || !valid_fmt(fmt)) return SQ_ERR_INVALID_ARG;
+    if (rows < 0 || K <= 0 || ld < K) return SQ_ERR_INVALID_ARG;
+    if (rows > (int64_t(1) << 40) || K > (int64_t(1) << 30) || ld > (int64_t(1) << 40)) return SQ_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(sf)) return SQ_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(x) & (dtype_size(dt) - 1)) != 0) return SQ_ERR_MISALIGNED;
+    if (rows == 0) return SQ_OK;
+    fp4::QuantArgs a{x, rows, K, ld, s, g, q, sf, 0, weight};
+    const cudaStream_t st = as_stream(stream);
+    const cudaError_t e = dt == SQ_F32   ? launch_quant_vec<DT_F32>(a, fmt, st)
+                          : dt == SQ_F16 ? launch_quant_vec<DT_F16>(a, fmt, st)
+                                         : launch_quant_vec<DT_BF16>(a, fmt, st);
+    return e == cudaSuccess ? check_launch() : cuda_fail(e);
+}
+
+template <int DT, int VEC>
+cudaError_t launch_dequant(fp4::DequantArgs a, int fmt, cudaStream_t st)
+{
+    const dim3 grid = strip_grid(a.rows, a.K, fp4::QTY, 8, a.slab), block(fp4::QTX, fp4::QTY);
+    if (fmt == SQ_MXFP4) return launch_pdl(fp4::k_fp4_dequant<DT, VEC, fp4::FMT_MX>, grid, block, 0, st, a);
+    return launch_pdl(fp4::k_fp4_dequant<DT, VEC, fp4::FMT_NV>, grid, block, 0, st, a);
+}
+
+template <int DT>
+cudaError_t launch_dequant_vec(const fp4::DequantArgs &a, int fmt, cudaStream_t st)
+{
+    const int vec = vec_bytes(a.out, a.K * dtype_size(DT));
+    if (vec == 32) return launch_dequant<DT, 32>(a, fmt, st);
+    if (vec == 16) return launch_dequant<DT, 16>(a, fmt, st);
+    return launch_dequant<DT, 0>(a, fmt, st);
+}
+
+// ------------------------------------------------------------------ product
+// Scale tiles of [rows, K] as a 3D tensor [row tiles][tiles along K][128 x
+// 4 bytes]; box: kt tiles along K of nb row tiles.  Tiles outside read as 0.
+bool make_scale_map(CUtensorMap *m, const void *base, int64_t ktiles, int64_t rows, uint32_t kt, uint32_t nb)
+{
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(ktiles), static_cast<cuuint64_t>(cdiv(rows, 128))};
+    cuuint64_t strides[2] = {fp4::SF_TILE, static_cast<cuuint64_t>(ktiles) * fp4::SF_TILE};
+    cuuint32_t box[3] = {128, kt, nb};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void *>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+struct Fp4Operands {
+    const void *xq, *xs, *wq, *ws;
+    int64_t row_bytes, ktiles;
+};
+
+template <int BN, int KBO, int CS, int FMT>
+sq_status launch_fp4_swap(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_t st)
+{
+    using C = fp4::SwapCfg<BN, KBO, FMT>;
+    CUtensorMap mw, mx, mws, mxs;
+    if constexpr (KBO == 1) {
+        if (!make_map(&mw, o.wq, false, o.row_bytes, fp.p.N, gemm::BM)) return SQ_ERR_CUDA;
+        if (!make_map(&mx, o.xq, false, o.row_bytes, fp.p.M, BN)) return SQ_ERR_CUDA;
+    } else {
+        if (!make_map3(&mw, o.wq, o.row_bytes, fp.p.N, gemm::BM, KBO)) return SQ_ERR_CUDA;
+        if (!make_map3(&mx, o.xq, o.row_bytes, fp.p.M, BN, KBO)) return SQ_ERR_CUDA;
+    }
+    const uint32_t kt = KBO * fp4::SfT<FMT>::TILES;
+    if (!make_scale_map(&mws, o.ws, o.ktiles, fp.p.N, kt, 1)) return SQ_ERR_CUDA;
+    if (!make_scale_map(&mxs, o.xs, o.ktiles, fp.p.M, kt, 1)) return SQ_ERR_CUDA;
+    gemm::Params &p = fp.p;
+    p.num_kb = static_cast<int>(cdiv(o.row_bytes, 128 * KBO));
+    p.sk_ctas = p.tiles_r;
+    p.sk_iters = p.tiles_r * p.num_kb;
+    p.timeout_ns = g_timeout_ns;
+    p.inject = g_inject & 1;
+    auto kern = fp4::k_fp4_swap<BN, KBO, CS, FMT>;
+    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), C::SMEM_BYTES);
+    if (e != cudaSuccess) return cuda_fail(e);
+    const dim3 grid(static_cast<unsigned>(p.tiles_r * CS));
+    if constexpr (CS > 1)
+        e = launch_pdl_cluster_smem(kern, grid, dim3(gemm::NUM_THREADS), CS, C::SMEM_BYTES, st, mw, mx, mws, mxs, fp);
+    else
+        e = launch_pdl(kern, grid, dim3(gemm::NUM_THREADS), C::SMEM_BYTES, st, mw, mx, mws, mxs, fp);
+    return e == cudaSuccess ? check_launch() : cuda_fail(e);
+}
+
+template <int BN, int KBO, int FMT>
+sq_status launch_fp4_swap_cs(const fp4::Fp4Params &fp, const Fp4Operands &o, int cs, cudaStream_t st)
+{
+    if (cs == 4) return launch_fp4_swap<BN, KBO, 4, FMT>(fp, o, st);
+    if (cs == 2) return launch_fp4_swap<BN, KBO, 2, FMT>(fp, o, st);
+    return launch_fp4_swap<BN, KBO, 1, FMT>(fp, o, st);
+}
+
+template <int KBO, int FMT>
+sq_status launch_fp4_swap_bn(const fp4::Fp4Params &fp, const Fp4Operands &o, int cs, cudaStream_t st)
+{
+    const int M = fp.p.M;
+    if (M <= 16) return launch_fp4_swap_cs<16, KBO, FMT>(fp, o, cs, st);
+    if (M <= 32) return launch_fp4_swap_cs<32, KBO, FMT>(fp, o, cs, st);
+    if (M <= 64) return launch_fp4_swap_cs<64, KBO, FMT>(fp, o, cs, st);
+    return launch_fp4_swap_cs<128, KBO, FMT>(fp, o, cs, st);
+}
+
+template <int FMT>
+sq_status dispatch_fp4_swap(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_t st)
+{
+    fp.p.tiles_r = static_cast<int>(cdiv(fp.p.N, gemm::BM));
+    fp.p.tiles_c = 1;
+    const bool kb2 = (o.row_bytes % 128) == 0;              // two K blocks a load (3D maps)
+    const int64_t groups = cdiv(o.row_bytes, kb2 ? 256 : 128);
+    if (static_cast<int64_t>(fp.p.tiles_r) * groups >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
+    // a cluster of 2 or 4 CTAs shares a tile's K range where one tile a CTA
+    // would leave more than half of the SMs idle, as in the INT8 kernel
+    int cs = 1;
+    if (2 * fp.p.tiles_r <= sm_count() && !(g_inject & 2)) {
+        const int64_t c = std::min<int64_t>(sm_count() / fp.p.tiles_r, groups);
+        cs = c >= 4 ? 4 : c >= 2 ? 2 : 1;
+    }
+    return kb2 ? launch_fp4_swap_bn<2, FMT>(fp, o, cs, st) : launch_fp4_swap_bn<1, FMT>(fp, o, cs, st);
+}
+
+template <int BN, int KBO, int FMT>
+sq_status launch_fp4_pair(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_t st)
+{
+    using C = fp4::Pair4Cfg<BN, KBO, FMT>;
+    gemm::Params &p = fp.p;
+    CUtensorMap ma, mb, mas, mbs, mo;
+    if constexpr (KBO == 1) {
+        if (!make_map(&ma, o.xq, false, o.row_bytes, p.M, gemm::BM)) return SQ_ERR_CUDA;
+        if (!make_map(&mb, o.wq, false, o.row_bytes, p.N, BN / 2)) return SQ_ERR_CUDA;
+    } else {
+        if (!make_map3(&ma, o.xq, o.row_bytes, p.M, gemm::BM, KBO)) return SQ_ERR_CUDA;
+        if (!make_map3(&mb, o.wq, o.row_bytes, p.N, BN / 2, KBO)) return SQ_ERR_CUDA;
+    }
+    const uint32_t kt = KBO * fp4::SfT<FMT>::TILES;
+    if (!make_scale_map(&mas, o.xs, o.ktiles, p.M, kt, 1)) return SQ_ERR_CUDA;
+    if (!make_scale_map(&mbs, o.ws, o.ktiles, p.N, kt, C::NB)) return SQ_ERR_CUDA;
+    std::memset(&mo, 0, sizeof(mo));
+    // TMA stores need 16-byte row strides and base
+    fp.direct = !aligned16(p.out) || (static_cast<int64_t>(p.N) * dtype_size(p.out_dt)) % 16 != 0;
+    if (!fp.direct && !make_out_map(&mo, p.out, p.out_dt, false, p.M, p.N)) return SQ_ERR_CUDA;
+    p.num_kb = static_cast<int>(cdiv(o.row_bytes, 128 * KBO));
+    const int64_t tr = cdiv(p.M, 2 * gemm::BM), tc = cdiv(p.N, BN);
+    if (tr * tc >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
+    p.tiles_r = static_cast<int>(tr);
+    p.tiles_c = static_cast<int>(tc);
+    p.num_units = static_cast<int>(tr * tc);
+    p.timeout_ns = g_timeout_ns;
+    p.inject = g_inject & 1;
+    auto kern = fp4::k_fp4_pair<BN, KBO, FMT>;
+    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), C::SMEM_BYTES);
+    if (e != cudaSuccess) return cuda_fail(e);
+    int max_clusters = 0;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        max_clusters = kinfo(reinterpret_cast<const void *>(kern)).clusters;
+    }
+    if (max_clusters == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * (sm_count() / 2), 1, 1);
+        cfg.blockDim = dim3(gemm::NUM_THREADS, 1, 1);
+        cfg.dynamicSmemBytes = C::SMEM_BYTES;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void *>(kern), &cfg) != cudaSuccess || n <= 0)
+            n = sm_count() / 2;
+        cudaGetLastError();
+        max_clusters = n;
+        std::lock_guard<std::mutex> lk(g_mu);
+        kinfo(reinterpret_cast<const void *>(kern)).clusters = n;
+    }
+    const int clusters = static_cast<int>(std::min<int64_t>(p.num_units, max_clusters));
+    e = launch_pdl(kern, dim3(2 * clusters), dim3(gemm::NUM_THREADS), C::SMEM_BYTES, st, ma, mb, mas, mbs, mo, fp);
+    return e == cudaSuccess ? check_launch() : cuda_fail(e);
+}
+
+template <int FMT>
+sq_status dispatch_fp4_pair(const fp4::Fp4Params &fp, const Fp4Operands &o, cudaStream_t st)
+{
+    // tile width with the fewest waves x width, a narrower tile charged for
+    // the operand bytes it moves per multiply
+    const int64_t clusters = std::max(1, sm_count() / 2);
+    const int cands[3] = {256, 192, 128};
+    const double eff[3] = {1.0, 0.85, 0.7};
+    int best = 256;
+    double best_cost = -1.0;
+    for (int i = 0; i < 3; ++i) {
+        const int64_t tiles = cdiv(fp.p.M, 2 * gemm::BM) * cdiv(fp.p.N, cands[i]);
+        const double cost = static_cast<double>(cdiv(tiles, clusters) * cands[i]) / eff[i];
+        if (best_cost < 0 || cost < best_cost) {
+            best = cands[i];
+            best_cost = cost;
+        }
+    }
+    switch (best) {
+    case 256: return launch_fp4_pair<256, 1, FMT>(fp, o, st);
+    case 192: return launch_fp4_pair<192, 1, FMT>(fp, o, st);
+    default: return launch_fp4_pair<128, 1, FMT>(fp, o, st);
+    }
+}
+
+// ------------------------------------------------------------------ key/value cache
+inline bool valid_kv(int f) { return f == SQ_KV_INT8 || f == SQ_KV_FP8 || f == SQ_KV_MXFP4; }
+
+// log2 of the lanes of a warp that share a row of D elements, 16 a lane
+inline int lanes_log2(int D)
+{
+    int l = 1;                                  // two lanes hold an MXFP4 block
+    while (l < 5 && (16 << l) < D) ++l;
+    return l;
+}
+
+
+#define SQ_KV_DISPATCH(KERN, FMTV, DTV, ARGS, GRID, ST)                                                    \
+    [&]() -> cudaError_t {                                                                                 \
+        auto by_fmt = [&](auto dtc, auto nchc) -> cudaError_t {                                            \
+            constexpr int DT_ = decltype(dtc)::value, NCH_ = decltype(nchc)::value;                        \
+            const dim3 blocks_(GRID), block(kv::WARPS * 32);                                               \
+            if ((FMTV) == SQ_KV_INT8) return launch_pdl(kv::KERN<DT_, kv::KV_INT8, NCH_>, blocks_, block, 0, ST, ARGS); \
+            if ((FMTV) == SQ_KV_FP8) return launch_pdl(kv::KERN<DT_, kv::KV_FP8, NCH_>, blocks_, block, 0, ST, ARGS);   \
+            return launch_pdl(kv::KERN<DT_, kv::KV_MXFP4, NCH_>, blocks_, block, 0, ST, ARGS);                \
+        };                                                                                                 \
+        auto by_chunks = [&](auto dtc) -> cudaError_t {                                                    \
+            if ((ARGS).D > 512) return by_fmt(dtc, std::integral_constant<int, 2>());                      \
+            return by_fmt(dtc, std::integral_constant<int, 1>());                                          \
+        };                                                                                                 \
+        if ((DTV) == SQ_F32) return by_chunks(std::integral_constant<int, DT_F32>());                      \
+        if ((DTV) == SQ_F16) return by_chunks(std::integral_constant<int, DT_F16>());                      \
+        return by_chunks(std::integral_constant<int, DT_BF16>());                                          \
+    }()
+
+sq_status check_kv(int fmt, int dt, int64_t H, int64_t D)
+{
+    if (!valid_kv(fmt) || !valid_dt(dt) || H <= 0 || D <= 0) return SQ_ERR_INVALID_ARG;
+    if (D > kv::MAX_D || H > 65536) return SQ_ERR_UNSUPPORTED;
+    return SQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sq_fp4_code_bytes(int64_t K) { return K > 0 ? static_cast<size_t>(fp4::code_row_bytes(K)) : 0; }
+
+size_t sq_fp4_scale_bytes(sq_fp4_format fmt, int64_t rows, int64_t K)
+{
+    if (!valid_fmt(fmt) || rows <= 0 || K <= 0) return 0;
+    return static_cast<size_t>(cdiv(rows, 128)) * static_cast<size_t>(fp4::scale_tiles_k(fmt, K)) * fp4::SF_TILE;
+}
+
+sq_status sq_smooth_scales_nvfp4(const float *act_max, const float *w_max, int64_t K, float alpha, float *s,
+                                 float *g_act, float *g_w, sq_stream stream)
+{
+    const sq_status r = sq_smooth_scales(act_max, w_max, K, alpha, s, nullptr, stream);
+    if (r != SQ_OK || (g_act == nullptr && g_w == nullptr)) return r;
+    const cudaError_t e = launch_pdl(fp4::k_nvfp4_scales, dim3(1), dim3(1024), 0, as_stream(stream), act_max, w_max, K,
+                                     static_cast<const float *>(s), g_act, g_w);
+    return e == cudaSuccess ? check_launch() : cuda_fail(e);
+}
+
+sq_status sq_quant_weight_fp4(const void *w, sq_dtype dt, int64_t N, int64_t K, const float *s, sq_fp4_format fmt,
+                              const float *g, uint8_t *wq4, uint8_t *w_sf, sq_stream stream)
+{
+    return quant_fp4(w, dt, N, K, K, s, 1, fmt, g, wq4, w_sf, stream);
+}
+
+sq_status sq_smooth_quant_act_fp4(const void *x, sq_dtype dt, int64_t M, int64_t K, int64_t ld, const float *s,
+                                  sq_fp4_format fmt, const float *g, uint8_t *xq4, uint8_t *x_sf, sq_stream stream)
+{
+    return quant_fp4(x, dt, M, K, ld, s, 0, fmt, g, xq4, x_sf, stream);
+}
+
+sq_status sq_dequant_fp4(const uint8_t *q4, const uint8_t *sf, sq_fp4_format fmt, int64_t rows, int64_t K,
+                         const float *g, sq_dtype out_dt, void *out, sq_stream stream)
+{
+    if (q4 == nullptr || sf == nullptr || out == nullptr || !valid_fmt(fmt) || !valid_dt(out_dt))
+        return SQ_ERR_INVALID_ARG;
+    if (rows < 0 || K <= 0) return SQ_ERR_INVALID_ARG;
+    if (rows > (int64_t(1) << 40) || K > (int64_t(1) << 30)) return SQ_ERR_UNSUPPORTED;
+    if (!aligned16(q4) || !aligned16(sf)) return SQ_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(out) & (dtype_size(out_dt) - 1)) != 0) return SQ_ERR_MISALIGNED;
+    if (rows == 0) return SQ_OK;
+    fp4::DequantArgs a{q4, sf, rows, K, g, out, 0};
+    const cudaStream_t st = as_stream(stream);
+    const cudaError_t e = out_dt == SQ_F32   ? launch_dequant_vec<DT_F32>(a, fmt, st)
+                          : out_dt == SQ_F16 ? launch_dequant_vec<DT_F16>(a, fmt, st)
+                                             : launch_dequant_vec<DT_BF16>(a, fmt, st);
+    return e == cudaSuccess ? check_launch() : cuda_fail(e);
+}
+
+sq_status sq_linear_fp4(const uint8_t *xq4, const uint8_t *x_sf, const uint8_t *wq4, const uint8_t *w_sf,
+                        sq_fp4_format fmt, int64_t M, int64_t N, int64_t K, const float *g_act, const float *g_w,
+                        const void *bias, sq_dtype out_dt, void *y, sq_stream stream)
+{
+    if (xq4 == nullptr || x_sf == nullptr || wq4 == nullptr || w_sf == nullptr || y == nullptr || !valid_fmt(fmt) ||
+        !valid_dt(out_dt))
+        return SQ_ERR_INVALID_ARG;
+    if (M < 0 || N <= 0 || K <= 0) return SQ_ERR_INVALID_ARG;
+    if (M > (int64_t(1) << 30) || N > (int64_t(1) << 30) || K > (int64_t(1) << 30)) return SQ_ERR_UNSUPPORTED;
+    if (!aligned16(xq4) || !aligned16(x_sf) || !aligned16(wq4) || !aligned16(w_sf)) return SQ_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(y) & (dtype_size(out_dt) - 1)) != 0 ||
+        (reinterpret_cast<uintptr_t>(bias) & (dtype_size(out_dt) - 1)) != 0)
+        return SQ_ERR_MISALIGNED;
+    if (M == 0) return SQ_OK;
+    fp4::Fp4Params fp{};
+    gemm::Params &p = fp.p;
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    p.K = static_cast<int>(K);
+    p.bias = bias;
+    p.out = y;
+    p.out_dt = out_dt;
+    fp.g_act = fmt == SQ_NVFP4 ? g_act : nullptr;
+    fp.g_w = fmt == SQ_NVFP4 ? g_w : nullptr;
+    const Fp4Operands o{xq4, x_sf, wq4, w_sf, fp4::code_row_bytes(K), fp4::scale_tiles_k(fmt, K)};
+    const cudaStream_t st = as_stream(stream);
+    if (M <= 128)
+        return fmt == SQ_MXFP4 ? dispatch_fp4_swap<fp4::FMT_MX>(fp, o, st) : dispatch_fp4_swap<fp4::FMT_NV>(fp, o, st);
+    return fmt == SQ_MXFP4 ? dispatch_fp4_pair<fp4::FMT_MX>(fp, o, st) : dispatch_fp4_pair<fp4::FMT_NV>(fp, o, st);
+}
+
+size_t sq_kv_row_bytes(sq_kv_format fmt, int64_t D)
+{
+    return valid_kv(fmt) && D > 0 && D <= kv::MAX_D ? static_cast<size_t>(kv::row_bytes(fmt, static_cast<int>(D))) : 0;
+}
+
+size_t sq_kv_scale_bytes(sq_kv_format fmt, int64_t D)
+{
+    return valid_kv(fmt) && D > 0 && D <= kv::MAX_D ? static_cast<size_t>(kv::scale_bytes(fmt, static_cast<int>(D))) : 0;
+}
+
+sq_status sq_kv_cache_write(const void *k, const void *v, sq_dtype dt, int64_t T, int64_t H, int64_t D, int64_t k_ld,
+                            int64_t v_ld, const int64_t *slots, sq_kv_format fmt, int64_t num_slots, void *k_cache,
+                            void *k_scale, void *v_cache, void *v_scale, sq_stream stream)
+{
+    const sq_status r = check_kv(fmt, dt, H, D);
+    if (r != SQ_OK) return r;
+    if (k == nullptr || v == nullptr || slots == nullptr || k_cache == nullptr || k_scale == nullptr ||
+        v_cache == nullptr || v_scale == nullptr)
+        return SQ_ERR_INVALID_ARG;
+    if (T < 0 || k_ld < H * D || v_ld < H * D || num_slots < 0) return SQ_ERR_INVALID_ARG;
+    if (num_slots > (int64_t(1) << 40) || k_ld > (int64_t(1) << 32) || v_ld > (int64_t(1) << 32))
+        return SQ_ERR_UNSUPPORTED;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale))
+        return SQ_ERR_MISALIGNED;
+    if (((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & (dtype_size(dt) - 1)) != 0 ||
+        (reinterpret_cast<uintptr_t>(slots) & 7) != 0)
+        return SQ_ERR_MISALIGNED;
+    if (T == 0) return SQ_OK;
+    const int ll = lanes_log2(static_cast<int>(D));
+    kv::WriteArgs a{k, v, T, k_ld, v_ld, num_slots, slots, static_cast<uint8_t *>(k_cache),
+                    static_cast<uint8_t *>(v_cache), k_scale, v_scale, static_cast<int>(H), static_cast<int>(D),
+                    static_cast<int>(cdiv(H, 32 >> ll)), ll, 0};
+    const int64_t grid = cdiv(T * 2 * a.groups, kv::WARPS);
+    if (T > (int64_t(1) << 31) || grid >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
+    const int es = dtype_size(dt);
+    a.vec = std::min(vec_bytes(k, (k_ld * es) | (D * es)), vec_bytes(v, (v_ld * es) | (D * es)));
+    const cudaStream_t st = as_stream(stream);
+    const cudaError_t e = SQ_KV_DISPATCH(k_kv_write, fmt, dt, a, static_cast<unsigned>(grid), st);
+    return e == cudaSuccess ? check_launch() : cuda_fail(e);
+}
+
+sq_status sq_kv_cache_read(sq_kv_format fmt, const void *k_cache, const void *k_scale, const void *v_cache,
+                           const void *v_scale, int64_t num_pages, int64_t page_size, int64_t H, int64_t D,
+                           const int32_t *table, int64_t B, int64_t max_pages, const int32_t *cu_rows,
+                           const int32_t *starts, int64_t total, sq_dtype out_dt, void *k_out, void *v_out,
+                           sq_stream stream)
+{
+    const sq_status r = check_kv(fmt, out_dt, H, D);
+    if (r != SQ_OK) return r;
+    if (k_cache == nullptr || k_scale == nullptr || v_cache == nullptr || v_scale == nullptr || table == nullptr ||
+        cu_rows == nullptr || k_out == nullptr || v_out == nullptr)
+        return SQ_ERR_INVALID_ARG;
+    if (num_pages < 0 || page_size <= 0 || B < 0 || max_pages < 0 || total < 0) return SQ_ERR_INVALID_ARG;
+    if (num_pages >= (int64_t(1) << 31) || page_size >= (int64_t(1) << 31) || B >= (int64_t(1) << 30) ||
+        max_pages >= (int64_t(1) << 31) || total >= (int64_t(1) << 31))
+        return SQ_ERR_UNSUPPORTED;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale))
+        return SQ_ERR_MISALIGNED;
+    if (((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & (dtype_size(out_dt) - 1)) != 0 ||
+        ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(cu_rows) |
+          reinterpret_cast<uintptr_t>(starts)) & 3) != 0)
+        return SQ_ERR_MISALIGNED;
+    if (total == 0 || B == 0) return SQ_OK;
+    const int ll = lanes_log2(static_cast<int>(D));
+    kv::ReadArgs a{static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), k_scale, v_scale,
+                   num_pages, max_pages, table, cu_rows, starts, total, k_out, v_out, static_cast<int>(B),
+                   static_cast<int>(H), static_cast<int>(D), static_cast<int>(cdiv(H, 32 >> ll)),
+                   static_cast<int>(page_size), ll, 0};
+    const int64_t grid = cdiv(total * a.groups, kv::WARPS);
+    if (grid >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
+    const int es = dtype_size(out_dt);
+    a.vec = std::min(vec_bytes(k_out, D * es), vec_bytes(v_out, D * es));
+    const cudaStream_t st = as_stream(stream);
+    const cudaError_t e = SQ_KV_DISPATCH(k_kv_read, fmt, out_dt, a, static_cast<unsigned>(grid), st);
+    return e == cudaSuccess ? check_launch() : cuda_fail(e);
+}
+
+}  // extern "C"
