@@ -83,6 +83,34 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr)
         asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
 
+// N words (4, 8 or 16) of this thread's TMEM lane from registers.
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t *r)
+{
+    if constexpr (N == 4)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                     "r"(r[2]), "r"(r[3])
+                     : "memory");
+    else if constexpr (N == 8)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    else
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+                     "%13, %14, %15, %16};" ::"r"(taddr),
+                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                     "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                     : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_all(uint32_t taddr, const uint32_t *r)
+{
+    constexpr int S = N % 16 == 0 ? 16 : N % 8 == 0 ? 8 : 4;
+#pragma unroll
+    for (int i = 0; i < N; i += S) tmem_st<S>(taddr + i, r + i);
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 template <int FMT, int CG>
 __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
                                         uint32_t sfb, uint32_t accumulate)
@@ -315,37 +343,47 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // shared columns first, and the next tile's MMAs start once they are free, so
 // the rest of the epilogue still overlaps them.
 // ---------------------------------------------------------------------------
+constexpr int PAIR_THREADS = 352;      // gemm.cuh's six warps, four scale warps, the scale producer
+
+constexpr int SF_BUFS_MX = 4, SF_BUFS_NV = 2;
+constexpr int SF_SLOTS_MIN(int fmt) { return fmt == FMT_MX ? 4 : 4; }
+
 template <int BN, int KBO, int FMT>
 struct Pair4Cfg {
     using Sf = SfT<FMT>;
     static constexpr int A_KB = BM * BKB, B_KB = (BN / 2) * BKB;
     static constexpr int A_BYTES = A_KB * KBO, B_BYTES = B_KB * KBO;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int NB = (BN % 128) == 0 ? BN / 128 : BN / 128 + 1;     // row tiles of B's scales
     static constexpr int SFA_BYTES = KBO * Sf::TILES * SF_TILE, SFB_BYTES = NB * SFA_BYTES;
-    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
-    static constexpr int STG_BUFS = 1;
-    static constexpr int STG_TOTAL = 4 * STG_BUFS * STG_BYTES;
+    static constexpr int SF_BYTES = SFA_BYTES + SFB_BYTES;                   // a scale slot
+    static constexpr int STG_TOTAL = 4 * STG_BYTES;         // a warp: two buffers of 16-bit rows, or one of 32-bit rows
     static constexpr int COLS_BYTES = 2 * 256 * 4;          // the tile's bias, two tiles
-    static constexpr int FIXED_BYTES = 1024 + STG_TOTAL + COLS_BYTES + 256;
-    static constexpr int STAGES_RAW = (227 * 1024 - FIXED_BYTES) / STAGE_BYTES;
+    static constexpr int FIXED_BYTES = 1024 + STG_TOTAL + COLS_BYTES + 512;
+    static constexpr int ROOM = 227 * 1024 - FIXED_BYTES;
+    static constexpr int STAGES_RAW = (ROOM - SF_SLOTS_MIN(FMT) * SF_BYTES) / STAGE_BYTES;
     static constexpr int STAGES = STAGES_RAW > 10 ? 10 : STAGES_RAW;
-    static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * STAGE_BYTES;
+    static constexpr int SLOTS_RAW = (ROOM - STAGES * STAGE_BYTES) / SF_BYTES;
+    static constexpr int SLOTS = SLOTS_RAW > 8 ? 8 : SLOTS_RAW;
+    static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * STAGE_BYTES + SLOTS * SF_BYTES;
     static constexpr int SFA_COLS = KBO * Sf::TILES * 4, SFB_COLS = NB * SFA_COLS;
-    static constexpr int SF_COLS = SFA_COLS + SFB_COLS;
-    static constexpr int ACC_STRIDE = (512 - SF_COLS - BN) / 32 * 32 < BN ? (512 - SF_COLS - BN) / 32 * 32 : BN;
+    static constexpr int SF_COLS = SFA_COLS + SFB_COLS;     // of one stage
+    static constexpr int SF_BUFS = FMT == FMT_MX ? SF_BUFS_MX : SF_BUFS_NV;
+    static constexpr int ACC_ROOM = (512 - SF_BUFS * SF_COLS - BN) / 32 * 32;
+    static constexpr int ACC_STRIDE = ACC_ROOM < BN ? ACC_ROOM : BN;
     static constexpr int OVERLAP = BN - ACC_STRIDE;         // a multiple of 32
     static constexpr int SF_COL0 = ACC_STRIDE + BN;
-    static constexpr int TMEM_COLS = gemm::pow2_at_least(SF_COL0 + SF_COLS, 32);
-    static_assert(STAGE_BYTES % 1024 == 0, "stage must keep 1024-byte alignment");
+    static constexpr int TMEM_COLS = gemm::pow2_at_least(SF_COL0 + SF_BUFS * SF_COLS, 32);
+    static_assert(STAGE_BYTES % 1024 == 0 && SF_BYTES % 128 == 0, "alignment of swizzled tiles and of scale slots");
     static_assert(BN % 64 == 0 && BN >= 128 && BN <= 256, "pair MMA N");
     static_assert(TMEM_COLS <= 512 && ACC_STRIDE > 0, "accumulators and scales must fit TMEM");
-    static_assert((2 * STAGES + 6) * 8 + 16 <= 256, "barrier area");
+    static_assert(SF_BUFS <= STAGES && SLOTS >= 2, "a scale buffer's MMAs are told done by their stage's barrier");
+    static_assert((2 * STAGES + 6 + 2 * SLOTS + SF_BUFS) * 8 + 16 <= 512, "barrier area");
 };
 
 // One 32-column chunk of an accumulator: factor, bias, rounding, store.
-template <int BN>
 __device__ __forceinline__ void epilogue_chunk(const Fp4Params &fp, const CUtensorMap *omap, const uint32_t (&r)[32],
-                                               int n0, int mrow0, int lane, uint32_t buf, bool first, float factor,
+                                               int n0, int mrow0, int lane, uint32_t stg, int &nstore, float factor,
                                                const float *bias_tile)
 {
     const Params &p = fp.p;
@@ -385,10 +423,15 @@ __device__ __forceinline__ void epilogue_chunk(const Fp4Params &fp, const CUtens
             w[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
     }
-    // the staging buffer is rewritten only once the store issued from it has
-    // finished reading shared memory
-    if (lane == 0 && !first) ptx::bulk_wait_read_0();
+    // a staging buffer (two of 16-bit rows, or one of 32-bit rows) is rewritten
+    // only once the store issued from it has finished reading shared memory
+    if (lane == 0) {
+        if (wide) ptx::bulk_wait_read_0();
+        else ptx::bulk_wait_read_1();
+    }
     __syncwarp();
+    const uint32_t buf = stg + (wide ? 0u : static_cast<uint32_t>(nstore & 1) * (STG_BYTES / 2));
+    ++nstore;
     const int pieces = wide ? 8 : 4;           // 128-byte rows, chunk ^= row & 7; or 64-byte rows, chunk ^= (row >> 1) & 3
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -409,7 +452,7 @@ __device__ __forceinline__ void epilogue_chunk(const Fp4Params &fp, const CUtens
 }
 
 template <int BN, int KBO, int FMT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
     k_fp4_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                const __grid_constant__ CUtensorMap map_as, const __grid_constant__ CUtensorMap map_bs,
                const __grid_constant__ CUtensorMap map_o, const Fp4Params fp)
@@ -421,7 +464,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S * C::STAGE_BYTES + C::STG_TOTAL + C::COLS_BYTES);
+    uint8_t *after = smem + S * C::STAGE_BYTES + C::SLOTS * C::SF_BYTES;       // behind the rings
+    uint64_t *bars = reinterpret_cast<uint64_t *>(after + C::STG_TOTAL + C::COLS_BYTES);
     const uint32_t bar0 = ptx::smem_addr(bars);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
@@ -429,12 +473,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * S + 2 + b); };
     const uint32_t done_bar = bar0 + 8u * (2 * S + 4);
     const uint32_t shared_bar = bar0 + 8u * (2 * S + 5);       // the shared accumulator columns are drained
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 6);
+    auto sf_full_bar = [&](int s) { return bar0 + 8u * (2 * S + 6 + s); };           // a slot of this CTA's scales is loaded
+    auto sf_empty_bar = [&](int s) { return bar0 + 8u * (2 * S + 6 + C::SLOTS + s); };
+    auto sf_ready_bar = [&](int b) { return bar0 + 8u * (2 * S + 6 + 2 * C::SLOTS + b); };   // both CTAs' scales are in TMEM
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 6 + 2 * C::SLOTS + C::SF_BUFS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *ok_flag = reinterpret_cast<volatile int *>(tmem_slot + 2);     // [2]
     const uint32_t sbase = ptx::smem_addr(smem);
-    const uint32_t stg_base = sbase + S * C::STAGE_BYTES;
-    float *cols = reinterpret_cast<float *>(smem + S * C::STAGE_BYTES + C::STG_TOTAL);   // [2][256] bias
+    const uint32_t sf_base = sbase + S * C::STAGE_BYTES;
+    const uint32_t stg_base = ptx::smem_addr(after);
+    float *cols = reinterpret_cast<float *>(after + C::STG_TOTAL);   // [2][256] bias
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = ptx::cluster_ctarank();
@@ -446,6 +494,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             ptx::mbar_init(full_bar(s), 1);
             ptx::mbar_init(empty_bar(s), 1);
         }
+        for (int s = 0; s < C::SLOTS; ++s) {
+            ptx::mbar_init(sf_full_bar(s), 1);
+            ptx::mbar_init(sf_empty_bar(s), 4);
+        }
+        for (int b = 0; b < C::SF_BUFS; ++b) ptx::mbar_init(sf_ready_bar(b), 8);
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(tfull_bar(b), 1);
             ptx::mbar_init(tempty_bar(b), 8);
@@ -493,7 +546,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                         if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), 2 * C::STAGE_BYTES);
                         const uint32_t fb = ptx::map_to_rank(full_bar(stage), 0);
                         const uint32_t sa = sbase + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
-                        const uint32_t ssa = sb + C::B_BYTES, ssb = ssa + C::SFA_BYTES;
                         if constexpr (KBO == 1) {
                             ptx::tma_load_2d_pair(sa, &map_a, fb, kb * BKB, ta * BM);
                             ptx::tma_load_2d_pair(sb, &map_b, fb, kb * BKB, yb);
@@ -501,8 +553,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                             ptx::tma_load_3d_pair(sa, &map_a, fb, 0, ta * BM, kb * KBO);
                             ptx::tma_load_3d_pair(sb, &map_b, fb, 0, yb, kb * KBO);
                         }
-                        ptx::tma_load_3d_pair(ssa, &map_as, fb, 0, kb * KBO * Sf::TILES, ta);
-                        ptx::tma_load_3d_pair(ssb, &map_bs, fb, 0, kb * KBO * Sf::TILES, tc * BN / 128);
                     }
                     ++issued;
                     if (++stage == S) { stage = 0; phase ^= 1u; }
@@ -524,9 +574,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (leader only)
         if (lane == 0 && leader) {
-            int stage = 0, local = 0;
-            uint32_t phase = 0;
-            const uint32_t sfa0 = tmem_base + C::SF_COL0, sfb0 = sfa0 + C::SFA_COLS;
+            int stage = 0, local = 0, buf = 0;
+            uint32_t phase = 0, bphase = 0;
             for (int u = cluster; u < p.num_units; u += nclusters, ++local) {
                 const int b = local & 1;
                 const uint32_t use = static_cast<uint32_t>(local >> 1) & 1u;
@@ -539,24 +588,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                 int tr, tc;
                 gemm::decode_unit(p, u, tr, tc);
                 // a tile that starts in the middle of a row tile of scales
-                // starts 2 columns (64 rows) into the copy
+                // starts 2 columns (64 rows) into it
                 const uint32_t shift = (BN % 128) != 0 ? static_cast<uint32_t>((tc * BN) % 128 / 32) : 0u;
                 bool ok = true;
                 for (int kb = 0; kb < p.num_kb; ++kb) {
-                    if (!ptx::wait_bounded(full_bar(stage), phase, tmo, abort_flag, ERR_MMA + 1)) {
+                    if (!ptx::wait_bounded(full_bar(stage), phase, tmo, abort_flag, ERR_MMA + 1) ||
+                        !ptx::wait_bounded(sf_ready_bar(buf), bphase, tmo, abort_flag, ERR_MMA + 3)) {
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after();
                     const uint32_t sa = sbase + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
-                    const uint32_t ssa = sb + C::B_BYTES, ssb = ssa + C::SFA_BYTES;
-#pragma unroll
-                    for (int i = 0; i < KBO * Sf::TILES; ++i) {
-                        copy_scales<2>(sfa0 + 4 * i, ssa + i * SF_TILE);
-#pragma unroll
-                        for (int t = 0; t < C::NB; ++t)
-                            copy_scales<2>(sfb0 + 4 * (i * C::NB + t), ssb + (t * KBO * Sf::TILES + i) * SF_TILE);
-                    }
+                    const uint32_t sfa0 = tmem_base + C::SF_COL0 + buf * C::SF_COLS, sfb0 = sfa0 + C::SFA_COLS;
 #pragma unroll
                     for (int j = 0; j < KBO; ++j) {
                         const uint64_t ad = ptx::sdesc_kmajor_sw128(sa + j * C::A_KB);
@@ -571,6 +614,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                     }
                     ptx::tc_commit_pair_mc(empty_bar(stage), 0x3);
                     if (++stage == S) { stage = 0; phase ^= 1u; }
+                    if (++buf == C::SF_BUFS) { buf = 0; bphase ^= 1u; }
                 }
                 if (!ok) break;
                 ptx::tc_commit_pair_mc(tfull_bar(b), 0x3);
@@ -579,13 +623,93 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             volatile int no_abort = 0;
             ptx::wait_bounded(done_bar, 0u, tmo, &no_abort, ERR_DRAIN + 1);
         }
+    } else if (warp == 10) {
+        // ------------------------------------------------ scale producer (both CTAs)
+        if (lane == 0) {
+            int slot = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int u = cluster; u < p.num_units && ok; u += nclusters) {
+                int tr, tc;
+                gemm::decode_unit(p, u, tr, tc);
+                const int ta = 2 * tr + static_cast<int>(rank);              // 128-row tile of A
+                for (int kb = 0; kb < p.num_kb; ++kb) {
+                    ok = ptx::wait_bounded(sf_empty_bar(slot), phase ^ 1u, tmo, abort_flag, ERR_PRODUCER + 1);
+                    if (!ok) break;
+                    const uint32_t fb = sf_full_bar(slot);
+                    const uint32_t ssa = sf_base + slot * C::SF_BYTES;
+                    ptx::mbar_arrive_expect_tx(fb, C::SF_BYTES);
+                    ptx::tma_load_3d(ssa, &map_as, fb, 0, kb * KBO * Sf::TILES, ta);
+                    ptx::tma_load_3d(ssa + C::SFA_BYTES, &map_bs, fb, 0, kb * KBO * Sf::TILES, tc * BN / 128);
+                    ++issued;
+                    if (++slot == C::SLOTS) { slot = 0; phase ^= 1u; }
+                }
+            }
+            const int n_wait = issued < C::SLOTS ? issued : C::SLOTS;
+            for (int i = 0; i < n_wait; ++i) {
+                int s = slot - 1 - i;
+                uint32_t ph = phase;
+                if (s < 0) { s += C::SLOTS; ph ^= 1u; }
+                volatile int no_abort = 0;
+                ptx::wait_bounded(sf_full_bar(s), ph, tmo, &no_abort, ERR_DRAIN + 2);
+            }
+        }
+    } else if (warp >= 6) {
+        // ------------------------------------------------ scales (warps 6..9, both CTAs)
+        // TMEM lane l of every quarter holds rows l, 32 + l, 64 + l, 96 + l of
+        // a scale tile: the 16 bytes at 16 * l.  Written from registers while
+        // the MMAs of earlier stages run.
+        const uint32_t tlane = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::SF_COL0;
+        int slot = 0, buf = 0, old = 0, n = 0; // stage `old` was SF_BUFS stages before stage n
+        uint32_t phase = 0, ophase = 0;
+        bool ok = true;
+        for (int u = cluster; u < p.num_units && ok; u += nclusters) {
+            for (int kb = 0; kb < p.num_kb; ++kb) {
+                ok = ptx::wait_bounded(sf_full_bar(slot), phase, tmo, abort_flag, ERR_MMA + 4);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const uint32_t ssa = sf_base + slot * C::SF_BYTES + lane * 16, ssb = ssa + C::SFA_BYTES;
+                uint32_t r[C::SF_COLS];
+                auto word4 = [](uint32_t *d, uint32_t a) {
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+                                 : "r"(a)
+                                 : "memory");
+                };
+#pragma unroll
+                for (int i = 0; i < KBO * Sf::TILES; ++i) {
+                    word4(r + 4 * i, ssa + i * SF_TILE);
+#pragma unroll
+                    for (int t = 0; t < C::NB; ++t)
+                        word4(r + C::SFA_COLS + 4 * (i * C::NB + t), ssb + (t * KBO * Sf::TILES + i) * SF_TILE);
+                }
+                if (n >= C::SF_BUFS) {         // the MMAs that read this buffer have completed
+                    ok = ptx::wait_bounded(empty_bar(old), ophase, tmo, abort_flag, ERR_MMA + 5);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (++old == S) { old = 0; ophase ^= 1u; }
+                    ptx::tc_fence_after();
+                }
+                ++n;
+                tmem_st_all<C::SF_COLS>(tlane + buf * C::SF_COLS, r);
+                tmem_st_wait();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::mbar_arrive_tmem(ptx::map_to_rank(sf_ready_bar(buf), 0));
+                    ptx::mbar_arrive(sf_empty_bar(slot));        // every lane's words have arrived in registers
+                }
+                if (++slot == C::SLOTS) { slot = 0; phase ^= 1u; }
+                if (++buf == C::SF_BUFS) buf = 0;
+            }
+        }
+        __syncwarp();
     } else {
         // ------------------------------------------------ epilogue (warps 2..5, both CTAs)
         const int q = warp & 3;
         const uint32_t stg = stg_base + static_cast<uint32_t>((warp - 2) * STG_BYTES);
         const float factor = out_factor(fp);
-        bool first = true;
-        int local = 0;
+        int local = 0, nstore = 0;
         for (int u = cluster; u < p.num_units; u += nclusters, ++local) {
             int tr, tc;
             gemm::decode_unit(p, u, tr, tc);
@@ -605,28 +729,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(b * C::ACC_STRIDE);
             const int mrow0 = (2 * tr + static_cast<int>(rank)) * BM + q * 32;
+            auto column = [&](int i) { return (C::OVERLAP > 0 && b == 0) ? BN / 32 - 1 - i : i; };
+            auto finish = [&](const uint32_t (&r)[32], int c) {
+                const int n0 = tc * BN + c * 32;
+                if (n0 < p.N) epilogue_chunk(fp, &map_o, r, n0, mrow0, lane, stg, nstore, factor, bias_tile + c * 32);
+            };
             // the columns shared with the other accumulator first: the last
             // ones of the first accumulator, the first ones of the second
-#pragma unroll 1
-            for (int i = 0; i < BN / 32; ++i) {
-                const int c = (C::OVERLAP > 0 && b == 0) ? BN / 32 - 1 - i : i;
-                uint32_t r[32];
-                ptx::tmem_ld32(tbase + c * 32, r);
+            constexpr int OV = C::OVERLAP / 32;
+            if constexpr (OV > 0) {
+                uint32_t r[OV][32];
+#pragma unroll
+                for (int i = 0; i < OV; ++i) ptx::tmem_ld32(tbase + column(i) * 32, r[i]);
                 ptx::tmem_ld_wait();
-                if (C::OVERLAP > 0 && i == C::OVERLAP / 32 - 1) {
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(shared_bar, 0));
-                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_tmem(ptx::map_to_rank(shared_bar, 0));
+#pragma unroll
+                for (int i = 0; i < OV; ++i) finish(r[i], column(i));
+            }
+#pragma unroll 1
+            for (int i = OV; i < BN / 32; ++i) {
+                uint32_t r[32];
+                ptx::tmem_ld32(tbase + column(i) * 32, r);
+                ptx::tmem_ld_wait();
                 if (i == BN / 32 - 1) {        // the accumulator is in registers
                     ptx::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(tempty_bar(b), 0));
+                    if (lane == 0) ptx::mbar_arrive_tmem(ptx::map_to_rank(tempty_bar(b), 0));
                 }
-                const int n0 = tc * BN + c * 32;
-                if (n0 >= p.N) continue;
-                epilogue_chunk<BN>(fp, &map_o, r, n0, mrow0, lane, stg, first, factor, bias_tile + c * 32);
-                first = false;
+                finish(r, column(i));
             }
         }
         if (lane == 0) ptx::bulk_wait_all();     // output stores complete before the CTA exits

@@ -236,7 +236,7 @@ sq_status launch_fp4_pair(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_t 
     if (max_clusters == 0) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * (sm_count() / 2), 1, 1);
-        cfg.blockDim = dim3(gemm::NUM_THREADS, 1, 1);
+        cfg.blockDim = dim3(fp4::PAIR_THREADS, 1, 1);
         cfg.dynamicSmemBytes = C::SMEM_BYTES;
         int n = 0;
         if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void *>(kern), &cfg) != cudaSuccess || n <= 0)
@@ -247,7 +247,7 @@ sq_status launch_fp4_pair(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_t 
         kinfo(reinterpret_cast<const void *>(kern)).clusters = n;
     }
     const int clusters = static_cast<int>(std::min<int64_t>(p.num_units, max_clusters));
-    e = launch_pdl(kern, dim3(2 * clusters), dim3(gemm::NUM_THREADS), C::SMEM_BYTES, st, ma, mb, mas, mbs, mo, fp);
+    e = launch_pdl(kern, dim3(2 * clusters), dim3(fp4::PAIR_THREADS), C::SMEM_BYTES, st, ma, mb, mas, mbs, mo, fp);
     return e == cudaSuccess ? check_launch() : cuda_fail(e);
 }
 

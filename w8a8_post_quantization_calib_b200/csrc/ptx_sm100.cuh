@@ -331,6 +331,15 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar)
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
+// Arrive on a barrier of either CTA of the cluster for work in tensor memory
+// only (reads or writes that tcgen05.wait has seen complete, ordered by the
+// tcgen05 fences around the barrier).  mbar_arrive_cluster also publishes this
+// thread's writes to memory at cluster scope, which takes ~0.8 us of its time.
+__device__ __forceinline__ void mbar_arrive_tmem(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
 // try_wait with cluster-scope acquire: writes that CTAs of the cluster made
 // before their release-arrive on this barrier are visible afterwards.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
