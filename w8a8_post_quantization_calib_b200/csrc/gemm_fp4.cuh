@@ -9,19 +9,25 @@
 // so an operand tile is the same 128-byte-swizzled K-major tile as for the
 // 8-bit kernels with twice the elements.  The scales are read from tensor
 // memory: a scale tile (128 rows x 4 blocks, 512 bytes, laid out as in
-// fp4.cuh) comes into shared memory by TMA with its operand's K block, and
-// tcgen05.cp copies it to 4 TMEM columns (row r at lane r % 32, column r / 32,
-// replicated to the four lane quarters).  The copy and the MMAs that read it
-// are issued by one thread and execute in order, so the columns need no
-// barrier.
+// fp4.cuh) comes into shared memory by TMA and takes 4 TMEM columns (row r at
+// lane r % 32, column r / 32, replicated to the four lane quarters).
 //
-// Roles, barriers and the two orientations are those of gemm.cuh:
 //   k_fp4_swap (M <= 128): the weights fill the 128-row MMA and stream once;
 //     a cluster of CS CTAs shares a tile's K range where tiles are few.
+//     Scales go to TMEM by tcgen05.cp: issued by the MMA's thread, executed in
+//     order with the MMAs, no barrier.  Roles and barriers are gemm.cuh's.
 //   k_fp4_pair (M > 128): CTA pairs (cta_group::2), 256 x BN tiles.  Each CTA
 //     loads its 128 rows of A and BN/2 rows of B, its rows' A scales and all
-//     BN rows' B scales (each SM scales its own 128 x BN accumulator).
+//     BN rows' B scales (each SM scales its own 128 x BN accumulator).  Four
+//     more warps bring the scales from their own shared-memory ring to TMEM
+//     (tcgen05.st): 12 scale tiles a K block of NVFP4 (6 of MXFP4) take 0.57
+//     us by tcgen05.cp, in the tensor pipe and in turn with the block's 0.29 us
+//     of MMAs.  M = 8192, N = 28672, K = 8192: 1165 -> 724 us (NVFP4), 850 ->
+//     708 us (MXFP4), then bound by power (5.3 PFLOP/s at ~1.5 GHz; 6.3 on
+//     all-zero codes, at 1965 MHz).
 #pragma once
+
+#include <type_traits>
 
 #include "fp4.cuh"
 #include "gemm.cuh"
@@ -73,14 +79,9 @@ __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr)
            (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
 }
 
-template <int CG>
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr)
 {
-    const uint64_t d = sdesc_scales(saddr);
-    if constexpr (CG == 1)
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
-    else
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc_scales(saddr)) : "memory");
 }
 
 // N words (4, 8 or 16) of this thread's TMEM lane from registers.
@@ -136,35 +137,58 @@ __device__ __forceinline__ float out_factor(const Fp4Params &fp)
 
 // ---------------------------------------------------------------------------
 // Small M: A = weights [N, K], B = activations [M, K] (M <= 128, one token
-// tile), one weight tile per cluster of CS CTAs.
+// tile); a TMEM lane is an output channel, a column a token.  A cluster of CS
+// CTAs shares a weight tile's K range; two CTAs fit an SM.  The partial sums
+// are reduced by the whole cluster: groups of four tokens are dealt out to the
+// CTAs in turn, and each CTA sends its part of a group to the group's owner
+// (st.async into the owner's stages, which its MMAs have finished with, counted
+// on the owner's barrier).  Sums are taken in the order own, then by rank.
 // ---------------------------------------------------------------------------
-template <int BN, int KBO, int FMT>
+template <int BN, int FMT>
 struct SwapCfg {
     using Sf = SfT<FMT>;
-    static constexpr int A_KB = BM * BKB, B_KB = BN * BKB;
-    static constexpr int A_BYTES = A_KB * KBO, B_BYTES = B_KB * KBO;
-    static constexpr int SF_BYTES = KBO * Sf::TILES * SF_TILE;     // of one operand's 128 rows
+    static constexpr int A_BYTES = BM * BKB, B_BYTES = BN * BKB;
+    static constexpr int SF_BYTES = Sf::TILES * SF_TILE;           // of one operand's 128 rows
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 2 * SF_BYTES;
-    static constexpr int STAGES_RAW = 220 * 1024 / STAGE_BYTES;
+    static constexpr int FIXED_BYTES = 1024 + 256;
+    static constexpr int STAGES_RAW = (112 * 1024 - FIXED_BYTES) / STAGE_BYTES;    // two CTAs an SM
     static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
-    static constexpr int SF_COLS = KBO * Sf::TILES * 4;
+    static constexpr int SF_COLS = Sf::TILES * 4;
     static constexpr int TMEM_COLS = gemm::pow2_at_least(BN + 2 * SF_COLS, 32);
-    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 512;
+    static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * STAGE_BYTES;
     static_assert(STAGE_BYTES % 1024 == 0, "stage must keep 1024-byte alignment");
-    static_assert((2 * STAGES + 4) * 8 + 16 <= 512, "barrier area");
-    static_assert(TMEM_COLS <= 512, "accumulator and scales must fit TMEM");
+    static_assert((2 * STAGES + 4) * 8 + 16 <= 256, "barrier area");
+    static_assert(TMEM_COLS <= 256, "accumulators and scales of two CTAs must fit TMEM");
 };
 
-template <int BN, int KBO, int CS, int FMT>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+// N consecutive columns (4 or 16) of this thread's TMEM lane
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N])
+{
+    if constexpr (N == 4)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(taddr)
+                     : "memory");
+    else
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                     "%14, %15}, [%16];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                       "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                     : "r"(taddr)
+                     : "memory");
+}
+
+template <int BN, int CS, int FMT>
+__global__ void __launch_bounds__(NUM_THREADS, 2)
     k_fp4_swap(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                const __grid_constant__ CUtensorMap map_ws, const __grid_constant__ CUtensorMap map_xs,
                const Fp4Params fp)
 {
-    using C = SwapCfg<BN, KBO, FMT>;
+    using C = SwapCfg<BN, FMT>;
     using Sf = SfT<FMT>;
     constexpr int S = C::STAGES;
-    static_assert((CS - 1) * BN * BM * 4 <= S * C::STAGE_BYTES, "partial sums must fit the leader's stages");
+    static_assert((CS - 1) * ((BN / 4 + CS - 1) / CS) * 2048 <= S * C::STAGE_BYTES, "partial sums must fit the stages");
     const Params &p = fp.p;
 
     extern __shared__ uint8_t smem_raw[];
@@ -175,15 +199,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
     const uint32_t tfull_bar = bar0 + 8u * (2 * S);
     const uint32_t done_bar = bar0 + 8u * (2 * S + 1);
-    const uint32_t go_bar = bar0 + 8u * (2 * S + 2);      // cluster split: leader's stages free
-    const uint32_t part_bar = bar0 + 8u * (2 * S + 3);    // cluster split: partial sums arrived
+    const uint32_t go_bar = bar0 + 8u * (2 * S + 2);      // every CTA of the cluster is done with its stages
+    const uint32_t part_bar = bar0 + 8u * (2 * S + 3);    // the others' partial sums have arrived
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 4);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *flag = reinterpret_cast<int *>(tmem_slot + 2);
-    __shared__ float s_am[BN];
     const uint32_t sbase = ptx::smem_addr(smem);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const int rank = CS > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
+    const int groups = (p.M + 3) >> 2;                     // of four tokens
+    auto owned = [&](int r) { return (groups - r + CS - 1) / CS; };      // groups r, r + CS, ...
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             ptx::mbar_init(full_bar(s), 1);
@@ -192,12 +217,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ptx::mbar_init(tfull_bar, 1);
         ptx::mbar_init(done_bar, 1);
         if constexpr (CS > 1) {
-            ptx::mbar_init(go_bar, 1);
-            ptx::mbar_init(part_bar, CS - 1);
+            ptx::mbar_init(go_bar, CS);
+            ptx::mbar_init(part_bar, 1);
         }
         *abort_flag = 0;
-        *flag = 0;
         ptx::fence_barrier_init();
+        if constexpr (CS > 1) ptx::mbar_arrive_expect_tx(part_bar, static_cast<uint32_t>((CS - 1) * owned(rank) * 2048));
     }
     if (warp == 0 && lane == 0) {
         ptx::tma_prefetch_desc(&map_w);
@@ -213,85 +238,80 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncthreads();
     if constexpr (CS > 1) ptx::cluster_sync();   // every CTA's barriers exist before any remote arrive
     ptx::tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const uint64_t tmo = p.timeout_ns;
-    // this CTA's share of its tile's K groups
-    const int tile = static_cast<int>(blockIdx.x) / CS, part = static_cast<int>(blockIdx.x) % CS;
-    const int kb_begin = static_cast<int>(static_cast<int64_t>(part) * p.num_kb / CS);
-    const int kb_end = static_cast<int>(static_cast<int64_t>(part + 1) * p.num_kb / CS);
+    // this CTA's share of its tile's K blocks
+    const int tile = static_cast<int>(blockIdx.x) / CS;
+    const int kb_begin = static_cast<int>(static_cast<int64_t>(rank) * p.num_kb / CS);
+    const int kb_end = static_cast<int>(static_cast<int64_t>(rank + 1) * p.num_kb / CS);
     pdl_wait();                        // operands and scales come from the previous kernels
 
+    // producer and MMA issuer walk their loops as whole warps (see k_fp4_pair)
+    const bool issuer = ptx::elect_one();
+    auto wait = [&](uint32_t bar, uint32_t parity, unsigned code) {
+        return __all_sync(0xffffffffu, ptx::wait_bounded(bar, parity, tmo, abort_flag, code));
+    };
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
-        if (lane == 0) {
-            int stage = 0, issued = 0;
-            uint32_t phase = 0;
-            for (int kb = kb_begin; kb < kb_end && !*abort_flag; ++kb) {
-                if (!ptx::wait_bounded(empty_bar(stage), phase ^ 1u, tmo, abort_flag, ERR_PRODUCER)) break;
-                const bool withhold = p.inject == 1 && blockIdx.x == 0 && issued == 0;
-                if (!withhold) {
-                    const uint32_t fb = full_bar(stage);
-                    ptx::mbar_arrive_expect_tx(fb, C::STAGE_BYTES);
-                    const uint32_t sa = sbase + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
-                    const uint32_t ssa = sb + C::B_BYTES, ssb = ssa + C::SF_BYTES;
-                    if constexpr (KBO == 1) {
-                        ptx::tma_load_2d(sa, &map_w, fb, kb * BKB, tile * BM);
-                        ptx::tma_load_2d(sb, &map_x, fb, kb * BKB, 0);
-                    } else {
-                        ptx::tma_load_3d(sa, &map_w, fb, 0, tile * BM, kb * KBO);
-                        ptx::tma_load_3d(sb, &map_x, fb, 0, 0, kb * KBO);
-                    }
-                    ptx::tma_load_3d(ssa, &map_ws, fb, 0, kb * KBO * Sf::TILES, tile);
-                    ptx::tma_load_3d(ssb, &map_xs, fb, 0, kb * KBO * Sf::TILES, 0);
-                }
-                ++issued;
-                if (++stage == S) { stage = 0; phase ^= 1u; }
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        for (int kb = kb_begin; kb < kb_end; ++kb) {
+            if (!wait(empty_bar(stage), phase ^ 1u, ERR_PRODUCER)) break;
+            const bool withhold = p.inject == 1 && blockIdx.x == 0 && issued == 0;
+            if (issuer && !withhold) {
+                const uint32_t fb = full_bar(stage);
+                ptx::mbar_arrive_expect_tx(fb, C::STAGE_BYTES);
+                const uint32_t sa = sbase + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
+                const uint32_t ssa = sb + C::B_BYTES, ssb = ssa + C::SF_BYTES;
+                ptx::tma_load_2d(sa, &map_w, fb, kb * BKB, tile * BM);
+                ptx::tma_load_3d(ssa, &map_ws, fb, 0, kb * Sf::TILES, tile);
+                ptx::tma_load_2d(sb, &map_x, fb, kb * BKB, 0);
+                ptx::tma_load_3d(ssb, &map_xs, fb, 0, kb * Sf::TILES, 0);
             }
-            // drain: every issued load lands before the CTA exits
-            const int n_wait = issued < S ? issued : S;
-            for (int i = 0; i < n_wait; ++i) {
-                int s = stage - 1 - i;
-                uint32_t ph = phase;
-                if (s < 0) { s += S; ph ^= 1u; }
-                volatile int no_abort = 0;
-                ptx::wait_bounded(full_bar(s), ph, tmo, &no_abort, ERR_DRAIN);
-            }
+            __syncwarp();
+            ++issued;
+            if (++stage == S) { stage = 0; phase ^= 1u; }
+        }
+        // drain: every issued load lands before the CTA exits
+        const int n_wait = issued < S ? issued : S;
+        for (int i = 0; i < n_wait; ++i) {
+            int s = stage - 1 - i;
+            uint32_t ph = phase;
+            if (s < 0) { s += S; ph ^= 1u; }
+            volatile int no_abort = 0;
+            ptx::wait_bounded(full_bar(s), ph, tmo, &no_abort, ERR_DRAIN);
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            const uint32_t sfa0 = tmem_base + BN, sfb0 = sfa0 + C::SF_COLS;
-            for (int kb = kb_begin; kb < kb_end; ++kb) {
-                if (!ptx::wait_bounded(full_bar(stage), phase, tmo, abort_flag, ERR_MMA + 1)) {
-                    ok = false;
-                    break;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const uint32_t sfa0 = tmem_base + BN, sfb0 = sfa0 + C::SF_COLS;
+        for (int kb = kb_begin; kb < kb_end; ++kb) {
+            ok = wait(full_bar(stage), phase, ERR_MMA + 1);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint32_t sa = sbase + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
+            const uint32_t ssa = sb + C::B_BYTES, ssb = ssa + C::SF_BYTES;
+            if (issuer) {
+#pragma unroll
+                for (int i = 0; i < Sf::TILES; ++i) {
+                    copy_scales(sfa0 + 4 * i, ssa + i * SF_TILE);
+                    copy_scales(sfb0 + 4 * i, ssb + i * SF_TILE);
                 }
-                ptx::tc_fence_after();
-                const uint32_t sa = sbase + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
-                const uint32_t ssa = sb + C::B_BYTES, ssb = ssa + C::SF_BYTES;
+                const uint64_t ad = ptx::sdesc_kmajor_sw128(sa), bd = ptx::sdesc_kmajor_sw128(sb);
 #pragma unroll
-                for (int i = 0; i < KBO * Sf::TILES; ++i) {
-                    copy_scales<1>(sfa0 + 4 * i, ssa + i * SF_TILE);
-                    copy_scales<1>(sfb0 + 4 * i, ssb + i * SF_TILE);
-                }
-#pragma unroll
-                for (int j = 0; j < KBO; ++j) {
-                    const uint64_t ad = ptx::sdesc_kmajor_sw128(sa + j * C::A_KB);
-                    const uint64_t bd = ptx::sdesc_kmajor_sw128(sb + j * C::B_KB);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int t = j * Sf::TILES + k / Sf::MMAS;
-                        mma_fp4<FMT, 1>(tmem_base, ad + 2 * k, bd + 2 * k,
-                                        idesc_fp4<FMT>(128, BN, (k % Sf::MMAS) * 2), sfa0 + 4 * t, sfb0 + 4 * t,
-                                        (kb > kb_begin || j > 0 || k > 0) ? 1u : 0u);
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const int t = k / Sf::MMAS;
+                    mma_fp4<FMT, 1>(tmem_base, ad + 2 * k, bd + 2 * k, idesc_fp4<FMT>(128, BN, (k % Sf::MMAS) * 2),
+                                    sfa0 + 4 * t, sfb0 + 4 * t, (kb > kb_begin || k > 0) ? 1u : 0u);
                 }
                 ptx::tc_commit(empty_bar(stage));
-                if (++stage == S) { stage = 0; phase ^= 1u; }
             }
+            __syncwarp();
+            if (++stage == S) { stage = 0; phase ^= 1u; }
+        }
+        if (issuer) {
             if (ok) ptx::tc_commit(tfull_bar);
             // drain: all issued MMAs complete before TMEM is released
             ptx::tc_commit(done_bar);
@@ -300,33 +320,84 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
     } else {
         // ------------------------------------------------ epilogue (warps 2..5)
-        const int q = warp & 3;
-        for (int m = threadIdx.x - 64; m < BN; m += 128) s_am[m] = 1.0f;
-        const int n = tile * BM + q * 32 + lane;
+        const int q = warp & 3, r = q * 32 + lane, n = tile * BM + r;
         const float factor = out_factor(fp);
         const float bn = n < p.N ? gemm::load_bias(p.bias, p.out_dt, n) : 0.0f;
-        ptx::named_bar_sync(1, 128);
-        auto tfull_wait = [&]() {
-            int ok = 1;
-            if (lane == 0) ok = ptx::wait_bounded(tfull_bar, 0u, tmo, abort_flag, ERR_EPI) ? 1 : 0;
-            return __shfl_sync(0xffffffffu, ok, 0) != 0;
+        auto emit = [&](int m, float acc) {
+            if (n < p.N && m < p.M)
+                gemm::store_out(p.out, p.out_dt, static_cast<int64_t>(m) * p.N + n, gemm::dequant(acc, factor, p.bias, bn));
         };
         const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-        if constexpr (CS > 1)
-            gemm::epilogue_cs<BN, gemm::EPI_DEQUANT, CS, gemm::KIND_F8>(p, tbase, tile, 0, q, lane,
-                                                                       ptx::cluster_ctarank(), factor, bn, s_am,
-                                                                       tfull_wait, go_bar, part_bar, sbase, abort_flag);
-        else
-            gemm::epilogue_sk<BN, gemm::EPI_DEQUANT, gemm::KIND_F8>(p, tbase, tile, 0, tile, q, lane, flag, abort_flag,
-                                                                    factor, bn, s_am, tfull_wait);
+        bool ok = wait(tfull_bar, 0u, ERR_EPI);
+        ptx::tc_fence_after();
+        if constexpr (CS == 1) {
+            if (ok) {
+#pragma unroll 1
+                for (int c = 0; c < p.M; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld<16>(tbase + c, v);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) emit(c + i, __uint_as_float(v[i]));
+                }
+            }
+        } else {
+            // [sender][owned group][row][4 tokens] in the owner's stages
+            if (ok && q == 2 && lane < CS) ptx::mbar_arrive_plain(ptx::map_to_rank(go_bar, lane));
+            ok = ok && wait(go_bar, 0u, ERR_EPI + 4);
+            if (ok) {
+#pragma unroll 1
+                for (int c = 0; c < groups; c += 4) {
+                    uint32_t v[16];
+                    tmem_ld<16>(tbase + c * 4, v);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int g = c + i, owner = g % CS;
+                        if (g < groups && owner != rank) {
+                            const int slot = rank < owner ? rank : rank - 1;
+                            const uint32_t off = static_cast<uint32_t>(((slot * owned(owner) + g / CS) * BM + r) * 16);
+                            ptx::st_async_v4(ptx::map_to_rank(sbase + off, owner), ptx::map_to_rank(part_bar, owner), v[4 * i],
+                                             v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        }
+                    }
+                }
+                ok = __all_sync(0xffffffffu, ptx::wait_bounded_cluster(part_bar, 0u, tmo, abort_flag, ERR_EPI + 3));
+            }
+            if (ok) {
+                const int mine = owned(rank);
+#pragma unroll 1
+                for (int j = 0; j < mine; ++j) {
+                    const int m = (j * CS + rank) * 4;
+                    uint32_t v[4];
+                    tmem_ld<4>(tbase + m, v);
+                    ptx::tmem_ld_wait();
+                    float acc[4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) acc[t] = __uint_as_float(v[t]);
+#pragma unroll
+                    for (int s = 0; s < CS - 1; ++s) {
+                        float4 o;
+                        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(o.x), "=f"(o.y), "=f"(o.z), "=f"(o.w)
+                                     : "r"(sbase + static_cast<uint32_t>(((s * mine + j) * BM + r) * 16))
+                                     : "memory");
+                        acc[0] += o.x;
+                        acc[1] += o.y;
+                        acc[2] += o.z;
+                        acc[3] += o.w;
+                    }
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) emit(m + t, acc[t]);
+                }
+            }
+        }
         ptx::tc_fence_before();
     }
 
-    // warps 0 and 1 ran their role on lane 0 alone: reconverge them first
     __syncwarp();
-    ptx::tc_fence_before();
-    if constexpr (CS > 1) ptx::cluster_sync();   // no CTA leaves while another may still write to its stages
-    else __syncthreads();
+    __syncthreads();
+    if constexpr (CS > 1) ptx::cluster_meet();   // no CTA leaves while another may still write to its stages
     pdl_trigger();                     // every output of this CTA is written
     if (warp == 1) {
         __syncwarp();
@@ -337,7 +408,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
 // ---------------------------------------------------------------------------
 // Large M: CTA pairs, 256 x BN tiles.  TMEM holds two accumulators and the
-// scale columns of a stage.  256-wide tiles leave no room for two whole
+// scale columns of SF_BUFS stages.  256-wide tiles leave no room for two whole
 // accumulators beside the scales: the second starts ACC_STRIDE < BN columns
 // behind the first and shares OVERLAP columns with it.  The epilogue drains the
 // shared columns first, and the next tile's MMAs start once they are free, so
@@ -357,7 +428,7 @@ struct Pair4Cfg {
     static constexpr int NB = (BN % 128) == 0 ? BN / 128 : BN / 128 + 1;     // row tiles of B's scales
     static constexpr int SFA_BYTES = KBO * Sf::TILES * SF_TILE, SFB_BYTES = NB * SFA_BYTES;
     static constexpr int SF_BYTES = SFA_BYTES + SFB_BYTES;                   // a scale slot
-    static constexpr int STG_TOTAL = 4 * STG_BYTES;         // a warp: two buffers of 16-bit rows, or one of 32-bit rows
+    static constexpr int STG_TOTAL = 4 * 2 * STG_BYTES;     // two buffers a warp, 32 rows x 128 bytes each
     static constexpr int COLS_BYTES = 2 * 256 * 4;          // the tile's bias, two tiles
     static constexpr int FIXED_BYTES = 1024 + STG_TOTAL + COLS_BYTES + 512;
     static constexpr int ROOM = 227 * 1024 - FIXED_BYTES;
@@ -381,73 +452,111 @@ struct Pair4Cfg {
     static_assert((2 * STAGES + 6 + 2 * SLOTS + SF_BUFS) * 8 + 16 <= 512, "barrier area");
 };
 
-// One 32-column chunk of an accumulator: factor, bias, rounding, store.
-__device__ __forceinline__ void epilogue_chunk(const Fp4Params &fp, const CUtensorMap *omap, const uint32_t (&r)[32],
-                                               int n0, int mrow0, int lane, uint32_t stg, int &nstore, float factor,
-                                               const float *bias_tile)
+// Factor and bias of 32 accumulator columns, in place.
+template <bool BIAS>
+__device__ __forceinline__ void apply_factor(uint32_t (&r)[32], float factor, const float *bias_tile)
 {
-    const Params &p = fp.p;
-    float v[32];
+    if constexpr (BIAS) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-        const float4 b4 = *reinterpret_cast<const float4 *>(bias_tile + i);        // broadcast
-        const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
+        for (int i = 0; i < 32; i += 4) {
+            const float4 b4 = *reinterpret_cast<const float4 *>(bias_tile + i);    // broadcast
+            const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
-        for (int t = 0; t < 4; ++t) v[i + t] = gemm::dequant(__uint_as_float(r[i + t]), factor, p.bias, bb[t]);
-    }
-    if (fp.direct) {
-        const int m = mrow0 + lane;
-        if (m < p.M) {
-            const int nval = min(32, p.N - n0);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < nval) gemm::store_out(p.out, p.out_dt, static_cast<int64_t>(m) * p.N + n0 + i, v[i]);
-        }
-        return;
-    }
-    uint32_t w[32];
-    const bool wide = p.out_dt == DT_F32;
-    if (wide) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
-    } else if (p.out_dt == DT_F16) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            for (int t = 0; t < 4; ++t) r[i + t] = __float_as_uint(__fmaf_rn(__uint_as_float(r[i + t]), factor, bb[t]));
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&h);
-        }
+        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__fmul_rn(__uint_as_float(r[i]), factor));
     }
-    // a staging buffer (two of 16-bit rows, or one of 32-bit rows) is rewritten
-    // only once the store issued from it has finished reading shared memory
-    if (lane == 0) {
-        if (wide) ptx::bulk_wait_read_0();
-        else ptx::bulk_wait_read_1();
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack_out(uint32_t a, uint32_t b)
+{
+    if constexpr (DT == DT_F16) {
+        const __half2 h = __floats2half2_rn(__uint_as_float(a), __uint_as_float(b));
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(a), __uint_as_float(b));
+        return *reinterpret_cast<const uint32_t *>(&h);
     }
-    __syncwarp();
-    const uint32_t buf = stg + (wide ? 0u : static_cast<uint32_t>(nstore & 1) * (STG_BYTES / 2));
-    ++nstore;
-    const int pieces = wide ? 8 : 4;           // 128-byte rows, chunk ^= row & 7; or 64-byte rows, chunk ^= (row >> 1) & 3
+}
+
+// The accumulator at tbase (128 lanes x BN columns): factor, bias, rounding,
+// store, 64 columns a step; drained(i) is called when step i's columns are in
+// registers.  Outputs leave through a staging buffer of 32 rows x 128 bytes in
+// the output map's swizzle: 32 columns of 32-bit outputs, 64 of 16-bit ones.
+// The type and the bias are compile-time here: with run-time branches in every
+// chunk the epilogue took 3.4 us a 256-wide tile.
+template <int BN, int DT, bool BIAS, typename Drained>
+__device__ __forceinline__ void epilogue_pair(const Fp4Params &fp, const CUtensorMap *omap, uint32_t tbase, int ncol0,
+                                              int mrow0, int lane, uint32_t stg, int &nstore, float factor,
+                                              const float *bias_tile, bool reversed, Drained drained)
+{
+    const Params &p = fp.p;
+#pragma unroll 1
+    for (int i = 0; i < BN / 64; ++i) {
+        const int c = (reversed ? BN / 64 - 1 - i : i) * 64;
+        uint32_t r[2][32];
+        ptx::tmem_ld32(tbase + c, r[0]);
+        ptx::tmem_ld32(tbase + c + 32, r[1]);
+        ptx::tmem_ld_wait();
+        drained(i);
+        const int n0 = ncol0 + c;
+        if (n0 >= p.N) continue;
+        apply_factor<BIAS>(r[0], factor, bias_tile + c);
+        apply_factor<BIAS>(r[1], factor, bias_tile + c + 32);
+        if (fp.direct) {
+            // rows that no tensor map can describe: transposed through the
+            // staging buffer (rotated rows: no bank conflicts), a row a step
+            const int rows = min(32, p.M - mrow0);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        if (k < pieces) {
-            const uint32_t a = wide ? buf + lane * 128 + ((k ^ (lane & 7)) << 4)
-                                    : buf + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[4 * k]), "r"(w[4 * k + 1]),
-                         "r"(w[4 * k + 2]), "r"(w[4 * k + 3])
-                         : "memory");
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(stg + lane * 128 + ((j + lane) & 31) * 4), "r"(r[h][j]) : "memory");
+                __syncwarp();
+                const int n = n0 + 32 * h + lane;
+                if (n < p.N) {
+#pragma unroll 4
+                    for (int j = 0; j < rows; ++j) {
+                        float t;
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(t) : "r"(stg + j * 128 + ((j + lane) & 31) * 4) : "memory");
+                        gemm::store_out(p.out, DT, static_cast<int64_t>(mrow0 + j) * p.N + n, t);
+                    }
+                }
+                __syncwarp();
+            }
+            continue;
         }
-    }
-    ptx::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-        ptx::tma_store_2d(omap, buf, n0, mrow0);
-        ptx::bulk_commit();
+        constexpr int STORES = DT == DT_F32 ? 2 : 1;
+#pragma unroll
+        for (int h = 0; h < STORES; ++h) {
+            // a buffer is rewritten only once the store issued from it two
+            // stores ago has finished reading shared memory
+            if (lane == 0) ptx::bulk_wait_read_1();
+            __syncwarp();
+            const uint32_t buf = stg + static_cast<uint32_t>(nstore & 1) * STG_BYTES;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                uint32_t w[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    if constexpr (DT == DT_F32) w[t] = r[h][4 * k + t];
+                    else w[t] = pack_out<DT>(r[k / 4][8 * (k & 3) + 2 * t], r[k / 4][8 * (k & 3) + 2 * t + 1]);
+                }
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 128 + ((k ^ (lane & 7)) << 4)),
+                             "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                             : "memory");
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (DT != DT_F32 || n0 + 32 * h < p.N) ptx::tma_store_2d(omap, buf, n0 + 32 * h, mrow0);
+                ptx::bulk_commit();
+            }
+            ++nstore;
+        }
     }
 }
 
@@ -484,7 +593,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
     const uint32_t stg_base = ptx::smem_addr(after);
     float *cols = reinterpret_cast<float *>(after + C::STG_TOTAL);   // [2][256] bias
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = ptx::cluster_ctarank();
     const bool leader = (rank == 0);
     const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
@@ -521,68 +630,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
     ptx::tc_fence_before();
     ptx::cluster_sync();               // both CTAs' barriers exist before any remote use
     ptx::tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const uint64_t tmo = p.timeout_ns;
     pdl_wait();                        // operands and scales come from the previous kernels
 
+    // The producers and the MMA issuer walk their loops as whole warps, so that
+    // addresses and descriptors are warp-uniform (uniform registers feed these
+    // instructions); one elected lane issues.  With one lane walking alone a
+    // K block took 0.34 us however narrow the tile, against 0.27 us.
+    const bool issuer = ptx::elect_one();
+    auto wait = [&](uint32_t bar, uint32_t parity, unsigned code) {
+        return __all_sync(0xffffffffu, ptx::wait_bounded(bar, parity, tmo, abort_flag, code));
+    };
     if (warp == 0) {
         // ------------------------------------------------ TMA producer (both CTAs)
-        if (lane == 0) {
-            int stage = 0, issued = 0;
-            uint32_t phase = 0;
-            for (int u = cluster; u < p.num_units && !*abort_flag; u += nclusters) {
-                int tr, tc;
-                gemm::decode_unit(p, u, tr, tc);
-                bool ok = true;
-                const int ta = 2 * tr + static_cast<int>(rank);              // 128-row tile of A
-                const int yb = tc * BN + static_cast<int>(rank) * (BN / 2);
-                for (int kb = 0; kb < p.num_kb; ++kb) {
-                    if (!ptx::wait_bounded(empty_bar(stage), phase ^ 1u, tmo, abort_flag, ERR_PRODUCER)) {
-                        ok = false;
-                        break;
-                    }
-                    const bool withhold = p.inject == 1 && blockIdx.x == 0 && issued == 0;
-                    if (!withhold) {
-                        if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), 2 * C::STAGE_BYTES);
-                        const uint32_t fb = ptx::map_to_rank(full_bar(stage), 0);
-                        const uint32_t sa = sbase + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
-                        if constexpr (KBO == 1) {
-                            ptx::tma_load_2d_pair(sa, &map_a, fb, kb * BKB, ta * BM);
-                            ptx::tma_load_2d_pair(sb, &map_b, fb, kb * BKB, yb);
-                        } else {
-                            ptx::tma_load_3d_pair(sa, &map_a, fb, 0, ta * BM, kb * KBO);
-                            ptx::tma_load_3d_pair(sb, &map_b, fb, 0, yb, kb * KBO);
-                        }
-                    }
-                    ++issued;
-                    if (++stage == S) { stage = 0; phase ^= 1u; }
-                }
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int u = cluster; u < p.num_units && ok; u += nclusters) {
+            int tr, tc;
+            gemm::decode_unit(p, u, tr, tc);
+            const int ya = (2 * tr + static_cast<int>(rank)) * BM;
+            const int yb = tc * BN + static_cast<int>(rank) * (BN / 2);
+            for (int kb = 0; kb < p.num_kb; ++kb) {
+                ok = wait(empty_bar(stage), phase ^ 1u, ERR_PRODUCER);
                 if (!ok) break;
-            }
-            // drain: the leader's full barriers count both CTAs' bytes
-            if (leader) {
-                const int n_wait = issued < S ? issued : S;
-                for (int i = 0; i < n_wait; ++i) {
-                    int s = stage - 1 - i;
-                    uint32_t ph = phase;
-                    if (s < 0) { s += S; ph ^= 1u; }
-                    volatile int no_abort = 0;
-                    ptx::wait_bounded(full_bar(s), ph, tmo, &no_abort, ERR_DRAIN);
+                const bool withhold = p.inject == 1 && blockIdx.x == 0 && issued == 0;
+                if (issuer && !withhold) {
+                    if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), 2 * C::STAGE_BYTES);
+                    const uint32_t fb = ptx::map_to_rank(full_bar(stage), 0);
+                    const uint32_t sa = sbase + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
+                    if constexpr (KBO == 1) {
+                        ptx::tma_load_2d_pair(sa, &map_a, fb, kb * BKB, ya);
+                        ptx::tma_load_2d_pair(sb, &map_b, fb, kb * BKB, yb);
+                    } else {
+                        ptx::tma_load_3d_pair(sa, &map_a, fb, 0, ya, kb * KBO);
+                        ptx::tma_load_3d_pair(sb, &map_b, fb, 0, yb, kb * KBO);
+                    }
                 }
+                __syncwarp();
+                ++issued;
+                if (++stage == S) { stage = 0; phase ^= 1u; }
+            }
+        }
+        // drain: the leader's full barriers count both CTAs' bytes
+        if (leader) {
+            const int n_wait = issued < S ? issued : S;
+            for (int i = 0; i < n_wait; ++i) {
+                int s = stage - 1 - i;
+                uint32_t ph = phase;
+                if (s < 0) { s += S; ph ^= 1u; }
+                volatile int no_abort = 0;
+                ptx::wait_bounded(full_bar(s), ph, tmo, &no_abort, ERR_DRAIN);
             }
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (leader only)
-        if (lane == 0 && leader) {
+        if (leader) {
             int stage = 0, local = 0, buf = 0;
             uint32_t phase = 0, bphase = 0;
             for (int u = cluster; u < p.num_units; u += nclusters, ++local) {
                 const int b = local & 1;
                 const uint32_t use = static_cast<uint32_t>(local >> 1) & 1u;
-                if (!ptx::wait_bounded(tempty_bar(b), use ^ 1u, tmo, abort_flag, ERR_MMA)) break;
-                if (C::OVERLAP > 0 && local > 0 &&
-                    !ptx::wait_bounded(shared_bar, static_cast<uint32_t>(local - 1) & 1u, tmo, abort_flag, ERR_MMA + 2))
-                    break;
+                if (!wait(tempty_bar(b), use ^ 1u, ERR_MMA)) break;
+                if (C::OVERLAP > 0 && local > 0 && !wait(shared_bar, static_cast<uint32_t>(local - 1) & 1u, ERR_MMA + 2)) break;
                 ptx::tc_fence_after();
                 const uint32_t d = tmem_base + static_cast<uint32_t>(b * C::ACC_STRIDE);
                 int tr, tc;
@@ -592,67 +703,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
                 const uint32_t shift = (BN % 128) != 0 ? static_cast<uint32_t>((tc * BN) % 128 / 32) : 0u;
                 bool ok = true;
                 for (int kb = 0; kb < p.num_kb; ++kb) {
-                    if (!ptx::wait_bounded(full_bar(stage), phase, tmo, abort_flag, ERR_MMA + 1) ||
-                        !ptx::wait_bounded(sf_ready_bar(buf), bphase, tmo, abort_flag, ERR_MMA + 3)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = wait(sf_ready_bar(buf), bphase, ERR_MMA + 3) && wait(full_bar(stage), phase, ERR_MMA + 1);
+                    if (!ok) break;
                     ptx::tc_fence_after();
                     const uint32_t sa = sbase + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
-                    const uint32_t sfa0 = tmem_base + C::SF_COL0 + buf * C::SF_COLS, sfb0 = sfa0 + C::SFA_COLS;
+                    const uint32_t sfa0 = tmem_base + C::SF_COL0 + buf * C::SF_COLS, sfb0 = sfa0 + C::SFA_COLS + shift;
+                    if (issuer) {
 #pragma unroll
-                    for (int j = 0; j < KBO; ++j) {
-                        const uint64_t ad = ptx::sdesc_kmajor_sw128(sa + j * C::A_KB);
-                        const uint64_t bd = ptx::sdesc_kmajor_sw128(sb + j * C::B_KB);
+                        for (int j = 0; j < KBO; ++j) {
+                            const uint64_t ad = ptx::sdesc_kmajor_sw128(sa + j * C::A_KB);
+                            const uint64_t bd = ptx::sdesc_kmajor_sw128(sb + j * C::B_KB);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int t = j * Sf::TILES + k / Sf::MMAS;
-                            mma_fp4<FMT, 2>(d, ad + 2 * k, bd + 2 * k, idesc_fp4<FMT>(256, BN, (k % Sf::MMAS) * 2),
-                                            sfa0 + 4 * t, sfb0 + 4 * C::NB * t + shift,
-                                            (kb > 0 || j > 0 || k > 0) ? 1u : 0u);
+                            for (int k = 0; k < 4; ++k) {
+                                const int t = j * Sf::TILES + k / Sf::MMAS;
+                                mma_fp4<FMT, 2>(d, ad + 2 * k, bd + 2 * k, idesc_fp4<FMT>(256, BN, (k % Sf::MMAS) * 2),
+                                                sfa0 + 4 * t, sfb0 + 4 * C::NB * t, (kb > 0 || j > 0 || k > 0) ? 1u : 0u);
+                            }
                         }
+                        ptx::tc_commit_pair_mc(empty_bar(stage), 0x3);
                     }
-                    ptx::tc_commit_pair_mc(empty_bar(stage), 0x3);
+                    __syncwarp();
                     if (++stage == S) { stage = 0; phase ^= 1u; }
                     if (++buf == C::SF_BUFS) { buf = 0; bphase ^= 1u; }
                 }
                 if (!ok) break;
-                ptx::tc_commit_pair_mc(tfull_bar(b), 0x3);
+                if (issuer) ptx::tc_commit_pair_mc(tfull_bar(b), 0x3);
+                __syncwarp();
             }
-            ptx::tc_commit_pair(done_bar);
-            volatile int no_abort = 0;
-            ptx::wait_bounded(done_bar, 0u, tmo, &no_abort, ERR_DRAIN + 1);
+            if (issuer) {
+                ptx::tc_commit_pair(done_bar);
+                volatile int no_abort = 0;
+                ptx::wait_bounded(done_bar, 0u, tmo, &no_abort, ERR_DRAIN + 1);
+            }
         }
     } else if (warp == 10) {
         // ------------------------------------------------ scale producer (both CTAs)
-        if (lane == 0) {
-            int slot = 0, issued = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int u = cluster; u < p.num_units && ok; u += nclusters) {
-                int tr, tc;
-                gemm::decode_unit(p, u, tr, tc);
-                const int ta = 2 * tr + static_cast<int>(rank);              // 128-row tile of A
-                for (int kb = 0; kb < p.num_kb; ++kb) {
-                    ok = ptx::wait_bounded(sf_empty_bar(slot), phase ^ 1u, tmo, abort_flag, ERR_PRODUCER + 1);
-                    if (!ok) break;
+        int slot = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int u = cluster; u < p.num_units && ok; u += nclusters) {
+            int tr, tc;
+            gemm::decode_unit(p, u, tr, tc);
+            const int ta = 2 * tr + static_cast<int>(rank);                  // 128-row tile of A
+            for (int kb = 0; kb < p.num_kb; ++kb) {
+                ok = wait(sf_empty_bar(slot), phase ^ 1u, ERR_PRODUCER + 1);
+                if (!ok) break;
+                if (issuer) {
                     const uint32_t fb = sf_full_bar(slot);
                     const uint32_t ssa = sf_base + slot * C::SF_BYTES;
                     ptx::mbar_arrive_expect_tx(fb, C::SF_BYTES);
                     ptx::tma_load_3d(ssa, &map_as, fb, 0, kb * KBO * Sf::TILES, ta);
                     ptx::tma_load_3d(ssa + C::SFA_BYTES, &map_bs, fb, 0, kb * KBO * Sf::TILES, tc * BN / 128);
-                    ++issued;
-                    if (++slot == C::SLOTS) { slot = 0; phase ^= 1u; }
                 }
+                __syncwarp();
+                ++issued;
+                if (++slot == C::SLOTS) { slot = 0; phase ^= 1u; }
             }
-            const int n_wait = issued < C::SLOTS ? issued : C::SLOTS;
-            for (int i = 0; i < n_wait; ++i) {
-                int s = slot - 1 - i;
-                uint32_t ph = phase;
-                if (s < 0) { s += C::SLOTS; ph ^= 1u; }
-                volatile int no_abort = 0;
-                ptx::wait_bounded(sf_full_bar(s), ph, tmo, &no_abort, ERR_DRAIN + 2);
-            }
+        }
+        const int n_wait = issued < C::SLOTS ? issued : C::SLOTS;
+        for (int i = 0; i < n_wait; ++i) {
+            int s = slot - 1 - i;
+            uint32_t ph = phase;
+            if (s < 0) { s += C::SLOTS; ph ^= 1u; }
+            volatile int no_abort = 0;
+            ptx::wait_bounded(sf_full_bar(s), ph, tmo, &no_abort, ERR_DRAIN + 2);
         }
     } else if (warp >= 6) {
         // ------------------------------------------------ scales (warps 6..9, both CTAs)
@@ -665,8 +779,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
         bool ok = true;
         for (int u = cluster; u < p.num_units && ok; u += nclusters) {
             for (int kb = 0; kb < p.num_kb; ++kb) {
-                ok = ptx::wait_bounded(sf_full_bar(slot), phase, tmo, abort_flag, ERR_MMA + 4);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = wait(sf_full_bar(slot), phase, ERR_MMA + 4);
                 if (!ok) break;
                 const uint32_t ssa = sf_base + slot * C::SF_BYTES + lane * 16, ssb = ssa + C::SFA_BYTES;
                 uint32_t r[C::SF_COLS];
@@ -684,8 +797,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
                         word4(r + C::SFA_COLS + 4 * (i * C::NB + t), ssb + (t * KBO * Sf::TILES + i) * SF_TILE);
                 }
                 if (n >= C::SF_BUFS) {         // the MMAs that read this buffer have completed
-                    ok = ptx::wait_bounded(empty_bar(old), ophase, tmo, abort_flag, ERR_MMA + 5);
-                    ok = __all_sync(0xffffffffu, ok);
+                    ok = wait(empty_bar(old), ophase, ERR_MMA + 5);
                     if (!ok) break;
                     if (++old == S) { old = 0; ophase ^= 1u; }
                     ptx::tc_fence_after();
@@ -696,7 +808,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    ptx::mbar_arrive_tmem(ptx::map_to_rank(sf_ready_bar(buf), 0));
+                    ptx::mbar_arrive_plain(ptx::map_to_rank(sf_ready_bar(buf), 0));
                     ptx::mbar_arrive(sf_empty_bar(slot));        // every lane's words have arrived in registers
                 }
                 if (++slot == C::SLOTS) { slot = 0; phase ^= 1u; }
@@ -707,7 +819,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
     } else {
         // ------------------------------------------------ epilogue (warps 2..5, both CTAs)
         const int q = warp & 3;
-        const uint32_t stg = stg_base + static_cast<uint32_t>((warp - 2) * STG_BYTES);
+        const uint32_t stg = stg_base + static_cast<uint32_t>((warp - 2) * 2 * STG_BYTES);
         const float factor = out_factor(fp);
         int local = 0, nstore = 0;
         for (int u = cluster; u < p.num_units; u += nclusters, ++local) {
@@ -729,37 +841,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(b * C::ACC_STRIDE);
             const int mrow0 = (2 * tr + static_cast<int>(rank)) * BM + q * 32;
-            auto column = [&](int i) { return (C::OVERLAP > 0 && b == 0) ? BN / 32 - 1 - i : i; };
-            auto finish = [&](const uint32_t (&r)[32], int c) {
-                const int n0 = tc * BN + c * 32;
-                if (n0 < p.N) epilogue_chunk(fp, &map_o, r, n0, mrow0, lane, stg, nstore, factor, bias_tile + c * 32);
-            };
             // the columns shared with the other accumulator first: the last
             // ones of the first accumulator, the first ones of the second
-            constexpr int OV = C::OVERLAP / 32;
-            if constexpr (OV > 0) {
-                uint32_t r[OV][32];
-#pragma unroll
-                for (int i = 0; i < OV; ++i) ptx::tmem_ld32(tbase + column(i) * 32, r[i]);
-                ptx::tmem_ld_wait();
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_tmem(ptx::map_to_rank(shared_bar, 0));
-#pragma unroll
-                for (int i = 0; i < OV; ++i) finish(r[i], column(i));
-            }
-#pragma unroll 1
-            for (int i = OV; i < BN / 32; ++i) {
-                uint32_t r[32];
-                ptx::tmem_ld32(tbase + column(i) * 32, r);
-                ptx::tmem_ld_wait();
-                if (i == BN / 32 - 1) {        // the accumulator is in registers
+            auto drained = [&](int i) {
+                const bool shared = C::OVERLAP > 0 && i == (C::OVERLAP - 1) / 64, last = i == BN / 64 - 1;
+                if (shared || last) {
                     ptx::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive_tmem(ptx::map_to_rank(tempty_bar(b), 0));
+                    if (lane == 0 && shared) ptx::mbar_arrive_plain(ptx::map_to_rank(shared_bar, 0));
+                    if (lane == 0 && last) ptx::mbar_arrive_plain(ptx::map_to_rank(tempty_bar(b), 0));
                 }
-                finish(r, column(i));
-            }
+            };
+            auto run = [&](auto dt, auto bias) {
+                epilogue_pair<BN, decltype(dt)::value, decltype(bias)::value>(fp, &map_o, tbase, tc * BN, mrow0, lane, stg,
+                                                                              nstore, factor, bias_tile,
+                                                                              C::OVERLAP > 0 && b == 0, drained);
+            };
+            auto by_dt = [&](auto bias) {
+                if (p.out_dt == DT_BF16) run(std::integral_constant<int, DT_BF16>(), bias);
+                else if (p.out_dt == DT_F16) run(std::integral_constant<int, DT_F16>(), bias);
+                else run(std::integral_constant<int, DT_F32>(), bias);
+            };
+            if (p.bias != nullptr) by_dt(std::true_type());
+            else by_dt(std::false_type());
         }
         if (lane == 0) ptx::bulk_wait_all();     // output stores complete before the CTA exits
         __syncwarp();

@@ -124,36 +124,42 @@ bool make_scale_map(CUtensorMap *m, const void *base, int64_t ktiles, int64_t ro
     return r == CUDA_SUCCESS;
 }
 
+// Output map of the pair kernel's TMA stores: boxes of 32 rows x 128 bytes.
+bool make_out_map128(CUtensorMap *m, void *base, int out_dt, int64_t M, int64_t N)
+{
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    const CUtensorMapDataType t = out_dt == SQ_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                  : out_dt == SQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const int elt = dtype_size(out_dt);
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(N * elt)};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elt), 32};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, t, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Fp4Operands {
     const void *xq, *xs, *wq, *ws;
     int64_t row_bytes, ktiles;
 };
 
-template <int BN, int KBO, int CS, int FMT>
+template <int BN, int CS, int FMT>
 sq_status launch_fp4_swap(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_t st)
 {
-    using C = fp4::SwapCfg<BN, KBO, FMT>;
+    using C = fp4::SwapCfg<BN, FMT>;
+    constexpr uint32_t KT = fp4::SfT<FMT>::TILES;
     CUtensorMap mw, mx, mws, mxs;
-    if constexpr (KBO == 1) {
-        if (!make_map(&mw, o.wq, false, o.row_bytes, fp.p.N, gemm::BM)) return SQ_ERR_CUDA;
-        if (!make_map(&mx, o.xq, false, o.row_bytes, fp.p.M, BN)) return SQ_ERR_CUDA;
-    } else {
-        if (!make_map3(&mw, o.wq, o.row_bytes, fp.p.N, gemm::BM, KBO)) return SQ_ERR_CUDA;
-        if (!make_map3(&mx, o.xq, o.row_bytes, fp.p.M, BN, KBO)) return SQ_ERR_CUDA;
-    }
-    const uint32_t kt = KBO * fp4::SfT<FMT>::TILES;
-    if (!make_scale_map(&mws, o.ws, o.ktiles, fp.p.N, kt, 1)) return SQ_ERR_CUDA;
-    if (!make_scale_map(&mxs, o.xs, o.ktiles, fp.p.M, kt, 1)) return SQ_ERR_CUDA;
-    gemm::Params &p = fp.p;
-    p.num_kb = static_cast<int>(cdiv(o.row_bytes, 128 * KBO));
-    p.sk_ctas = p.tiles_r;
-    p.sk_iters = p.tiles_r * p.num_kb;
-    p.timeout_ns = g_timeout_ns;
-    p.inject = g_inject & 1;
-    auto kern = fp4::k_fp4_swap<BN, KBO, CS, FMT>;
+    if (!make_map(&mw, o.wq, false, o.row_bytes, fp.p.N, gemm::BM)) return SQ_ERR_CUDA;
+    if (!make_map(&mx, o.xq, false, o.row_bytes, fp.p.M, BN)) return SQ_ERR_CUDA;
+    if (!make_scale_map(&mws, o.ws, o.ktiles, fp.p.N, KT, 1)) return SQ_ERR_CUDA;
+    if (!make_scale_map(&mxs, o.xs, o.ktiles, fp.p.M, KT, 1)) return SQ_ERR_CUDA;
+    auto kern = fp4::k_fp4_swap<BN, CS, FMT>;
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), C::SMEM_BYTES);
     if (e != cudaSuccess) return cuda_fail(e);
-    const dim3 grid(static_cast<unsigned>(p.tiles_r * CS));
+    const dim3 grid(static_cast<unsigned>(fp.p.tiles_r * CS));
     if constexpr (CS > 1)
         e = launch_pdl_cluster_smem(kern, grid, dim3(gemm::NUM_THREADS), CS, C::SMEM_BYTES, st, mw, mx, mws, mxs, fp);
     else
@@ -161,40 +167,32 @@ sq_status launch_fp4_swap(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_t 
     return e == cudaSuccess ? check_launch() : cuda_fail(e);
 }
 
-template <int BN, int KBO, int FMT>
+template <int BN, int FMT>
 sq_status launch_fp4_swap_cs(const fp4::Fp4Params &fp, const Fp4Operands &o, int cs, cudaStream_t st)
 {
-    if (cs == 4) return launch_fp4_swap<BN, KBO, 4, FMT>(fp, o, st);
-    if (cs == 2) return launch_fp4_swap<BN, KBO, 2, FMT>(fp, o, st);
-    return launch_fp4_swap<BN, KBO, 1, FMT>(fp, o, st);
-}
-
-template <int KBO, int FMT>
-sq_status launch_fp4_swap_bn(const fp4::Fp4Params &fp, const Fp4Operands &o, int cs, cudaStream_t st)
-{
-    const int M = fp.p.M;
-    if (M <= 16) return launch_fp4_swap_cs<16, KBO, FMT>(fp, o, cs, st);
-    if (M <= 32) return launch_fp4_swap_cs<32, KBO, FMT>(fp, o, cs, st);
-    if (M <= 64) return launch_fp4_swap_cs<64, KBO, FMT>(fp, o, cs, st);
-    return launch_fp4_swap_cs<128, KBO, FMT>(fp, o, cs, st);
+    if (cs == 8) return launch_fp4_swap<BN, 8, FMT>(fp, o, st);
+    if (cs == 4) return launch_fp4_swap<BN, 4, FMT>(fp, o, st);
+    if (cs == 2) return launch_fp4_swap<BN, 2, FMT>(fp, o, st);
+    return launch_fp4_swap<BN, 1, FMT>(fp, o, st);
 }
 
 template <int FMT>
 sq_status dispatch_fp4_swap(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_t st)
 {
-    fp.p.tiles_r = static_cast<int>(cdiv(fp.p.N, gemm::BM));
-    fp.p.tiles_c = 1;
-    const bool kb2 = (o.row_bytes % 128) == 0;              // two K blocks a load (3D maps)
-    const int64_t groups = cdiv(o.row_bytes, kb2 ? 256 : 128);
-    if (static_cast<int64_t>(fp.p.tiles_r) * groups >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
-    // a cluster of 2 or 4 CTAs shares a tile's K range where one tile a CTA
-    // would leave more than half of the SMs idle, as in the INT8 kernel
+    gemm::Params &p = fp.p;
+    p.tiles_r = static_cast<int>(cdiv(p.N, gemm::BM));
+    p.num_kb = static_cast<int>(cdiv(o.row_bytes, 128));
+    p.timeout_ns = g_timeout_ns;
+    p.inject = g_inject & 1;
+    // the largest cluster whose CTAs all run at once (two an SM), with a K
+    // block each at least
     int cs = 1;
-    if (2 * fp.p.tiles_r <= sm_count() && !(g_inject & 2)) {
-        const int64_t c = std::min<int64_t>(sm_count() / fp.p.tiles_r, groups);
-        cs = c >= 4 ? 4 : c >= 2 ? 2 : 1;
-    }
-    return kb2 ? launch_fp4_swap_bn<2, FMT>(fp, o, cs, st) : launch_fp4_swap_bn<1, FMT>(fp, o, cs, st);
+    if (!(g_inject & 2))
+        while (cs < 8 && 2 * cs <= p.num_kb && static_cast<int64_t>(p.tiles_r) * 2 * cs <= 2 * sm_count()) cs *= 2;
+    if (p.M <= 16) return launch_fp4_swap_cs<16, FMT>(fp, o, cs, st);
+    if (p.M <= 32) return launch_fp4_swap_cs<32, FMT>(fp, o, cs, st);
+    if (p.M <= 64) return launch_fp4_swap_cs<64, FMT>(fp, o, cs, st);
+    return launch_fp4_swap_cs<128, FMT>(fp, o, cs, st);
 }
 
 template <int BN, int KBO, int FMT>
@@ -216,7 +214,7 @@ sq_status launch_fp4_pair(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_t 
     std::memset(&mo, 0, sizeof(mo));
     // TMA stores need 16-byte row strides and base
     fp.direct = !aligned16(p.out) || (static_cast<int64_t>(p.N) * dtype_size(p.out_dt)) % 16 != 0;
-    if (!fp.direct && !make_out_map(&mo, p.out, p.out_dt, false, p.M, p.N)) return SQ_ERR_CUDA;
+    if (!fp.direct && !make_out_map128(&mo, p.out, p.out_dt, p.M, p.N)) return SQ_ERR_CUDA;
     p.num_kb = static_cast<int>(cdiv(o.row_bytes, 128 * KBO));
     const int64_t tr = cdiv(p.M, 2 * gemm::BM), tc = cdiv(p.N, BN);
     if (tr * tc >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
@@ -254,16 +252,21 @@ sq_status launch_fp4_pair(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_t 
 template <int FMT>
 sq_status dispatch_fp4_pair(const fp4::Fp4Params &fp, const Fp4Operands &o, cudaStream_t st)
 {
-    // tile width with the fewest waves x width, a narrower tile charged for
-    // the operand bytes it moves per multiply
-    const int64_t clusters = std::max(1, sm_count() / 2);
+    // The tile width with the least estimated time: waves x (K blocks x time a
+    // block + time a tile), in us as measured on B200 over M = 129..4096, N =
+    // 1024..28672, K = 1024..11008.  A K block costs a narrow tile almost what
+    // it costs a wide one, so narrow tiles pay where they save a wave: M =
+    // 512, N = 12288, K = 4096 takes 16.7 / 14.9 / 19.0 us with 256 / 192 /
+    // 128 columns, M = 1024, N = 4096, K = 4096 11.4 / 14.8 / 14.7, M = 256,
+    // N = 4096, K = 1024 7.1 / 6.5 / 6.1.
+    const int64_t clusters = std::max(1, sm_count() / 2), kb = cdiv(o.row_bytes, 128);
     const int cands[3] = {256, 192, 128};
-    const double eff[3] = {1.0, 0.85, 0.7};
+    const double per_kb[3] = {0.35, 0.285, 0.275}, per_tile[3] = {1.1, 0.75, 0.35};
     int best = 256;
     double best_cost = -1.0;
     for (int i = 0; i < 3; ++i) {
         const int64_t tiles = cdiv(fp.p.M, 2 * gemm::BM) * cdiv(fp.p.N, cands[i]);
-        const double cost = static_cast<double>(cdiv(tiles, clusters) * cands[i]) / eff[i];
+        const double cost = static_cast<double>(cdiv(tiles, clusters)) * (static_cast<double>(kb) * per_kb[i] + per_tile[i]);
         if (best_cost < 0 || cost < best_cost) {
             best = cands[i];
             best_cost = cost;
