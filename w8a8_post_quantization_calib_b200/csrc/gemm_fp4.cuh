@@ -140,9 +140,10 @@ __device__ __forceinline__ float out_factor(const Fp4Params &fp)
 // tile); a TMEM lane is an output channel, a column a token.  A cluster of CS
 // CTAs shares a weight tile's K range; two CTAs fit an SM.  The partial sums
 // are reduced by the whole cluster: groups of four tokens are dealt out to the
-// CTAs in turn, and each CTA sends its part of a group to the group's owner
-// (st.async into the owner's stages, which its MMAs have finished with, counted
-// on the owner's barrier).  Sums are taken in the order own, then by rank.
+// CTAs in turn, and each is sent the others' sums of its own (st.async into its
+// stages, which its MMAs have finished with, counted on its barrier).  Sums are
+// taken in the order own, then by rank.  (Scales by tcgen05.st as in the pair
+// kernel were 0.2-0.6 us slower: these products wait for the weights.)
 // ---------------------------------------------------------------------------
 template <int BN, int FMT>
 struct SwapCfg {
@@ -151,13 +152,18 @@ struct SwapCfg {
     static constexpr int SF_BYTES = Sf::TILES * SF_TILE;           // of one operand's 128 rows
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 2 * SF_BYTES;
     static constexpr int FIXED_BYTES = 1024 + 256;
-    static constexpr int STAGES_RAW = (112 * 1024 - FIXED_BYTES) / STAGE_BYTES;    // two CTAs an SM
-    static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
+    static constexpr int MAX_STAGES = 10;
     static constexpr int SF_COLS = Sf::TILES * 4;
     static constexpr int TMEM_COLS = gemm::pow2_at_least(BN + 2 * SF_COLS, 32);
-    static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * STAGE_BYTES;
+    // stages and bytes of shared memory with one or two CTAs an SM
+    static constexpr int stages(int per_sm)
+    {
+        const int n = ((per_sm == 1 ? 224 : 112) * 1024 - FIXED_BYTES) / STAGE_BYTES;
+        return n < MAX_STAGES ? n : MAX_STAGES;
+    }
+    static constexpr int smem_bytes(int per_sm) { return FIXED_BYTES + stages(per_sm) * STAGE_BYTES; }
     static_assert(STAGE_BYTES % 1024 == 0, "stage must keep 1024-byte alignment");
-    static_assert((2 * STAGES + 4) * 8 + 16 <= 256, "barrier area");
+    static_assert((2 * MAX_STAGES + 4) * 8 + 16 <= 256, "barrier area");
     static_assert(TMEM_COLS <= 256, "accumulators and scales of two CTAs must fit TMEM");
 };
 
@@ -187,9 +193,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 2)
 {
     using C = SwapCfg<BN, FMT>;
     using Sf = SfT<FMT>;
-    constexpr int S = C::STAGES;
-    static_assert((CS - 1) * ((BN / 4 + CS - 1) / CS) * 2048 <= S * C::STAGE_BYTES, "partial sums must fit the stages");
+    static_assert((CS - 1) * ((BN / 4 + CS - 1) / CS) * 2048 <= C::stages(2) * C::STAGE_BYTES, "partial sums must fit the stages");
     const Params &p = fp.p;
+    const int S = p.ring;                                  // stages
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -322,26 +328,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 2)
         // ------------------------------------------------ epilogue (warps 2..5)
         const int q = warp & 3, r = q * 32 + lane, n = tile * BM + r;
         const float factor = out_factor(fp);
-        const float bn = n < p.N ? gemm::load_bias(p.bias, p.out_dt, n) : 0.0f;
-        auto emit = [&](int m, float acc) {
-            if (n < p.N && m < p.M)
-                gemm::store_out(p.out, p.out_dt, static_cast<int64_t>(m) * p.N + n, gemm::dequant(acc, factor, p.bias, bn));
-        };
+        // without a bias -0.0: the multiply-add then is the rounded product, sign of zero included
+        const float bn = p.bias != nullptr && n < p.N ? gemm::load_bias(p.bias, p.out_dt, n) : -0.0f;
         const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
         bool ok = wait(tfull_bar, 0u, ERR_EPI);
         ptx::tc_fence_after();
-        if constexpr (CS == 1) {
-            if (ok) {
-#pragma unroll 1
-                for (int c = 0; c < p.M; c += 16) {
-                    uint32_t v[16];
-                    tmem_ld<16>(tbase + c, v);
-                    ptx::tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) emit(c + i, __uint_as_float(v[i]));
-                }
-            }
-        } else {
+        if constexpr (CS > 1) {
             // [sender][owned group][row][4 tokens] in the owner's stages
             if (ok && q == 2 && lane < CS) ptx::mbar_arrive_plain(ptx::map_to_rank(go_bar, lane));
             ok = ok && wait(go_bar, 0u, ERR_EPI + 4);
@@ -364,33 +356,56 @@ __global__ void __launch_bounds__(NUM_THREADS, 2)
                 }
                 ok = __all_sync(0xffffffffu, ptx::wait_bounded_cluster(part_bar, 0u, tmo, abort_flag, ERR_EPI + 3));
             }
-            if (ok) {
-                const int mine = owned(rank);
+        }
+        // this CTA's groups, four a step, with the output's type known at compile time
+        const int mine = owned(rank);
+        auto emit = [&](auto dt) {
+            constexpr int DT = decltype(dt)::value;
+            constexpr int SZ = dtype_size(DT);
+            uint8_t *out = static_cast<uint8_t *>(p.out) + (static_cast<int64_t>(rank) * 4 * p.N + n) * SZ;
+            const int64_t token = static_cast<int64_t>(p.N) * SZ;
 #pragma unroll 1
-                for (int j = 0; j < mine; ++j) {
-                    const int m = (j * CS + rank) * 4;
-                    uint32_t v[4];
-                    tmem_ld<4>(tbase + m, v);
-                    ptx::tmem_ld_wait();
-                    float acc[4];
+            for (int j = 0; j < mine; j += 4) {
+                uint32_t v[4][4];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) acc[t] = __uint_as_float(v[t]);
+                for (int i = 0; i < 4; ++i) tmem_ld<4>(tbase + (min(j + i, mine - 1) * CS + rank) * 4, v[i]);
+                ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int s = 0; s < CS - 1; ++s) {
-                        float4 o;
-                        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                     : "=f"(o.x), "=f"(o.y), "=f"(o.z), "=f"(o.w)
-                                     : "r"(sbase + static_cast<uint32_t>(((s * mine + j) * BM + r) * 16))
-                                     : "memory");
-                        acc[0] += o.x;
-                        acc[1] += o.y;
-                        acc[2] += o.z;
-                        acc[3] += o.w;
+                for (int i = 0; i < 4; ++i) {
+                    if (j + i < mine) {
+                        float acc[4];
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) acc[t] = __uint_as_float(v[i][t]);
+#pragma unroll
+                        for (int s = 0; s < CS - 1; ++s) {
+                            float4 o;
+                            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                         : "=f"(o.x), "=f"(o.y), "=f"(o.z), "=f"(o.w)
+                                         : "r"(sbase + static_cast<uint32_t>(((s * mine + j + i) * BM + r) * 16))
+                                         : "memory");
+                            acc[0] += o.x;
+                            acc[1] += o.y;
+                            acc[2] += o.z;
+                            acc[3] += o.w;
+                        }
+                        const int left = n < p.N ? p.M - ((j + i) * CS + rank) * 4 : 0;
+                        if (left >= 4) {
+#pragma unroll
+                            for (int t = 0; t < 4; ++t) gemm::store_out(out + t * token, DT, 0, __fmaf_rn(acc[t], factor, bn));
+                        } else {
+#pragma unroll
+                            for (int t = 0; t < 3; ++t)
+                                if (t < left) gemm::store_out(out + t * token, DT, 0, __fmaf_rn(acc[t], factor, bn));
+                        }
+                        out += 4 * CS * token;
                     }
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) emit(m + t, acc[t]);
                 }
             }
+        };
+        if (ok) {
+            if (p.out_dt == DT_BF16) emit(std::integral_constant<int, DT_BF16>());
+            else if (p.out_dt == DT_F16) emit(std::integral_constant<int, DT_F16>());
+            else emit(std::integral_constant<int, DT_F32>());
         }
         ptx::tc_fence_before();
     }

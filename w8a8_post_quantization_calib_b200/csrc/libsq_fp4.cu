@@ -156,14 +156,17 @@ sq_status launch_fp4_swap(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_t 
     if (!make_map(&mx, o.xq, false, o.row_bytes, fp.p.M, BN)) return SQ_ERR_CUDA;
     if (!make_scale_map(&mws, o.ws, o.ktiles, fp.p.N, KT, 1)) return SQ_ERR_CUDA;
     if (!make_scale_map(&mxs, o.xs, o.ktiles, fp.p.M, KT, 1)) return SQ_ERR_CUDA;
-    auto kern = fp4::k_fp4_swap<BN, CS, FMT>;
-    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), C::SMEM_BYTES);
-    if (e != cudaSuccess) return cuda_fail(e);
     const dim3 grid(static_cast<unsigned>(fp.p.tiles_r * CS));
+    const int per_sm = static_cast<int64_t>(grid.x) <= sm_count() ? 1 : 2;
+    const int smem = C::smem_bytes(per_sm);
+    fp.p.ring = C::stages(per_sm);
+    auto kern = fp4::k_fp4_swap<BN, CS, FMT>;
+    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), smem);
+    if (e != cudaSuccess) return cuda_fail(e);
     if constexpr (CS > 1)
-        e = launch_pdl_cluster_smem(kern, grid, dim3(gemm::NUM_THREADS), CS, C::SMEM_BYTES, st, mw, mx, mws, mxs, fp);
+        e = launch_pdl_cluster_smem(kern, grid, dim3(gemm::NUM_THREADS), CS, smem, st, mw, mx, mws, mxs, fp);
     else
-        e = launch_pdl(kern, grid, dim3(gemm::NUM_THREADS), C::SMEM_BYTES, st, mw, mx, mws, mxs, fp);
+        e = launch_pdl(kern, grid, dim3(gemm::NUM_THREADS), smem, st, mw, mx, mws, mxs, fp);
     return e == cudaSuccess ? check_launch() : cuda_fail(e);
 }
 
@@ -184,11 +187,14 @@ sq_status dispatch_fp4_swap(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_
     p.num_kb = static_cast<int>(cdiv(o.row_bytes, 128));
     p.timeout_ns = g_timeout_ns;
     p.inject = g_inject & 1;
-    // the largest cluster whose CTAs all run at once (two an SM), with a K
-    // block each at least
+    // the largest cluster that leaves one CTA an SM and two K blocks a CTA: a
+    // second CTA an SM only adds partial sums (M = 128, N = 4096, K = 4096:
+    // 10.2 / 8.2 / 7.2 / 10.0 us with clusters of 1 / 2 / 4 / 8; M = 1, N =
+    // 11008: 6.4 with 1, 7.0 with 2; M = 1, N = 512, K = 512: 2.7 with 1, 3.3
+    // with 2), as from about 90 CTAs on the weights come at HBM's rate
     int cs = 1;
     if (!(g_inject & 2))
-        while (cs < 8 && 2 * cs <= p.num_kb && static_cast<int64_t>(p.tiles_r) * 2 * cs <= 2 * sm_count()) cs *= 2;
+        while (cs < 8 && 4 * cs <= p.num_kb && static_cast<int64_t>(p.tiles_r) * 2 * cs <= sm_count()) cs *= 2;
     if (p.M <= 16) return launch_fp4_swap_cs<16, FMT>(fp, o, cs, st);
     if (p.M <= 32) return launch_fp4_swap_cs<32, FMT>(fp, o, cs, st);
     if (p.M <= 64) return launch_fp4_swap_cs<64, FMT>(fp, o, cs, st);
