@@ -38,23 +38,24 @@ inline int vec_bytes(const void *p, int64_t ld_bytes)
     return (a & 31) == 0 ? 32 : (a & 15) == 0 ? 16 : 0;
 }
 
-// Column strips of 512 x slabs of rows: enough blocks for `per_sm` a SM, a
-// slab no shorter than one pass of the block.
-inline dim3 strip_grid(int64_t rows, int64_t cols, int pass, int per_sm, int64_t &slab)
+// two blocks of the quantiser fit an SM (one pass over the SMs), about two of
+// the dequantiser: measured best of 2, 3, 4, 6, 8
+constexpr int QUANT_PER_SM = 2, DEQUANT_PER_SM = 4;
+
+// Column strips of 512 x units of rows, at most `per_sm` blocks a SM.
+inline dim3 strip_grid(int64_t units, int64_t cols, int per_sm)
 {
     const int64_t gx = cdiv(cols, 16 * fp4::QTX);
-    const int64_t target = std::max<int64_t>(1, cdiv(static_cast<int64_t>(sm_count()) * per_sm, gx));
-    int64_t gy = std::max<int64_t>(1, std::min<int64_t>(cdiv(rows, pass), target));
-    gy = std::min<int64_t>(gy, 65535);
-    slab = cdiv(rows, gy);
-    return dim3(static_cast<unsigned>(gx), static_cast<unsigned>(cdiv(rows, slab)));
+    const int64_t target = std::max<int64_t>(1, static_cast<int64_t>(sm_count()) * per_sm / gx);
+    return dim3(static_cast<unsigned>(gx), static_cast<unsigned>(std::min<int64_t>(std::min(units, target), 65535)));
 }
 
 template <int DT, int VEC, int FMT>
 cudaError_t launch_quant(fp4::QuantArgs a, cudaStream_t st)
 {
     const int64_t cols = fp4::scale_tiles_k(FMT, a.K) * fp4::FmtT<FMT>::TILE_K;    // every byte of the scale tiles
-    const dim3 grid = strip_grid(a.rows, cols, fp4::QTY, 8, a.slab);
+    a.units = fp4::quant_units(a.rows);
+    const dim3 grid = strip_grid(a.units, cols, QUANT_PER_SM);
     return launch_pdl(fp4::k_fp4_quant<DT, VEC, FMT>, grid, dim3(fp4::QTX, fp4::QTY), 0, st, a);
 }
 
@@ -93,7 +94,8 @@ sq_status quant_fp4(const void *x, int dt, int64_t rows, int64_t K, int64_t ld, 
 template <int DT, int VEC>
 cudaError_t launch_dequant(fp4::DequantArgs a, int fmt, cudaStream_t st)
 {
-    const dim3 grid = strip_grid(a.rows, a.K, fp4::QTY, 8, a.slab), block(fp4::QTX, fp4::QTY);
+    a.units = fp4::quant_units(a.rows);
+    const dim3 grid = strip_grid(a.units, a.K, DEQUANT_PER_SM), block(fp4::QTX, fp4::QTY);
     if (fmt == SQ_MXFP4) return launch_pdl(fp4::k_fp4_dequant<DT, VEC, fp4::FMT_MX>, grid, block, 0, st, a);
     return launch_pdl(fp4::k_fp4_dequant<DT, VEC, fp4::FMT_NV>, grid, block, 0, st, a);
 }
@@ -296,24 +298,28 @@ inline int lanes_log2(int D)
     return l;
 }
 
+// Calls launch(type, format, chunks of 16 elements a lane, tokens a warp) with
+// all four as compile-time constants.
+template <typename F> cudaError_t kv_dispatch(int dt, int fmt, int D, bool many, F &&launch)
+{
+    auto tokens = [&](auto d, auto f) -> cudaError_t {
+        using std::integral_constant;
+        if (D > 512) return launch(d, f, integral_constant<int, 2>(), integral_constant<int, 1>());
+        if (many) return launch(d, f, integral_constant<int, 1>(), integral_constant<int, kv::TOKENS>());
+        return launch(d, f, integral_constant<int, 1>(), integral_constant<int, 1>());
+    };
+    auto format = [&](auto d) -> cudaError_t {
+        if (fmt == SQ_KV_INT8) return tokens(d, std::integral_constant<int, kv::KV_INT8>());
+        if (fmt == SQ_KV_FP8) return tokens(d, std::integral_constant<int, kv::KV_FP8>());
+        return tokens(d, std::integral_constant<int, kv::KV_MXFP4>());
+    };
+    if (dt == SQ_F32) return format(std::integral_constant<int, DT_F32>());
+    if (dt == SQ_F16) return format(std::integral_constant<int, DT_F16>());
+    return format(std::integral_constant<int, DT_BF16>());
+}
 
-#define SQ_KV_DISPATCH(KERN, FMTV, DTV, ARGS, GRID, ST)                                                    \
-    [&]() -> cudaError_t {                                                                                 \
-        auto by_fmt = [&](auto dtc, auto nchc) -> cudaError_t {                                            \
-            constexpr int DT_ = decltype(dtc)::value, NCH_ = decltype(nchc)::value;                        \
-            const dim3 blocks_(GRID), block(kv::WARPS * 32);                                               \
-            if ((FMTV) == SQ_KV_INT8) return launch_pdl(kv::KERN<DT_, kv::KV_INT8, NCH_>, blocks_, block, 0, ST, ARGS); \
-            if ((FMTV) == SQ_KV_FP8) return launch_pdl(kv::KERN<DT_, kv::KV_FP8, NCH_>, blocks_, block, 0, ST, ARGS);   \
-            return launch_pdl(kv::KERN<DT_, kv::KV_MXFP4, NCH_>, blocks_, block, 0, ST, ARGS);                \
-        };                                                                                                 \
-        auto by_chunks = [&](auto dtc) -> cudaError_t {                                                    \
-            if ((ARGS).D > 512) return by_fmt(dtc, std::integral_constant<int, 2>());                      \
-            return by_fmt(dtc, std::integral_constant<int, 1>());                                          \
-        };                                                                                                 \
-        if ((DTV) == SQ_F32) return by_chunks(std::integral_constant<int, DT_F32>());                      \
-        if ((DTV) == SQ_F16) return by_chunks(std::integral_constant<int, DT_F16>());                      \
-        return by_chunks(std::integral_constant<int, DT_BF16>());                                          \
-    }()
+// Several tokens a warp once that leaves every SM its 64 warps
+inline bool many_tokens(int64_t warps) { return warps >= static_cast<int64_t>(kv::TOKENS) * 64 * sm_count(); }
 
 sq_status check_kv(int fmt, int dt, int64_t H, int64_t D)
 {
@@ -437,12 +443,16 @@ sq_status sq_kv_cache_write(const void *k, const void *v, sq_dtype dt, int64_t T
     kv::WriteArgs a{k, v, T, k_ld, v_ld, num_slots, slots, static_cast<uint8_t *>(k_cache),
                     static_cast<uint8_t *>(v_cache), k_scale, v_scale, static_cast<int>(H), static_cast<int>(D),
                     static_cast<int>(cdiv(H, 32 >> ll)), ll, 0};
-    const int64_t grid = cdiv(T * 2 * a.groups, kv::WARPS);
-    if (T > (int64_t(1) << 31) || grid >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
+    if (T > (int64_t(1) << 31) || cdiv(T * 2 * a.groups, kv::WARPS) >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
     const int es = dtype_size(dt);
     a.vec = std::min(vec_bytes(k, (k_ld * es) | (D * es)), vec_bytes(v, (v_ld * es) | (D * es)));
     const cudaStream_t st = as_stream(stream);
-    const cudaError_t e = SQ_KV_DISPATCH(k_kv_write, fmt, dt, a, static_cast<unsigned>(grid), st);
+    const cudaError_t e = kv_dispatch(dt, fmt, a.D, many_tokens(T * 2 * a.groups), [&](auto d, auto f, auto nch, auto tok) {
+        constexpr int TOK = decltype(tok)::value;
+        const dim3 grid(static_cast<unsigned>(cdiv(cdiv(T, TOK) * 2 * a.groups, kv::WARPS)));
+        return launch_pdl(kv::k_kv_write<decltype(d)::value, decltype(f)::value, decltype(nch)::value, TOK>, grid,
+                          dim3(kv::WARPS * 32), 0, st, a);
+    });
     return e == cudaSuccess ? check_launch() : cuda_fail(e);
 }
 
@@ -473,12 +483,16 @@ sq_status sq_kv_cache_read(sq_kv_format fmt, const void *k_cache, const void *k_
                    num_pages, max_pages, table, cu_rows, starts, total, k_out, v_out, static_cast<int>(B),
                    static_cast<int>(H), static_cast<int>(D), static_cast<int>(cdiv(H, 32 >> ll)),
                    static_cast<int>(page_size), ll, 0};
-    const int64_t grid = cdiv(total * a.groups, kv::WARPS);
-    if (grid >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
+    if (cdiv(total * a.groups, kv::WARPS) >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
     const int es = dtype_size(out_dt);
     a.vec = std::min(vec_bytes(k_out, D * es), vec_bytes(v_out, D * es));
     const cudaStream_t st = as_stream(stream);
-    const cudaError_t e = SQ_KV_DISPATCH(k_kv_read, fmt, out_dt, a, static_cast<unsigned>(grid), st);
+    const cudaError_t e = kv_dispatch(out_dt, fmt, a.D, many_tokens(total * a.groups), [&](auto d, auto f, auto nch, auto tok) {
+        constexpr int TOK = decltype(tok)::value;
+        const dim3 grid(static_cast<unsigned>(cdiv(cdiv(total, TOK) * a.groups, kv::WARPS)));
+        return launch_pdl(kv::k_kv_read<decltype(d)::value, decltype(f)::value, decltype(nch)::value, TOK>, grid,
+                          dim3(kv::WARPS * 32), 0, st, a);
+    });
     return e == cudaSuccess ? check_launch() : cuda_fail(e);
 }
 
