@@ -124,7 +124,7 @@ __device__ __forceinline__ uint32_t block_scale(float m, float gc, float g, floa
     }
 }
 
-// 16 elements as they lie in memory: VEC bytes a load (32 or 16; 0: one by one)
+// 16 elements as they lie in memory
 template <int DT> struct Raw16 { uint4 v[dtype_size(DT)]; };
 
 __device__ __forceinline__ void load32(const void *p, uint4 &a, uint4 &b)
@@ -141,41 +141,84 @@ __device__ __forceinline__ void store32(void *p, const uint4 &a, const uint4 &b)
                  : "memory");
 }
 
-// Elements [c, c + 16) of the row at `row`; those at n and behind are 0.
+// VEC bytes (16, 8 or 4) as 32-bit words
+template <int VEC>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w)
+{
+    if constexpr (VEC == 16) {
+        const uint4 t = __ldg(reinterpret_cast<const uint4 *>(p));
+        w[0] = t.x;
+        w[1] = t.y;
+        w[2] = t.z;
+        w[3] = t.w;
+    } else if constexpr (VEC == 8) {
+        const uint2 t = __ldg(reinterpret_cast<const uint2 *>(p));
+        w[0] = t.x;
+        w[1] = t.y;
+    } else {
+        w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_words(uint8_t *p, const uint32_t *w)
+{
+    if constexpr (VEC == 16) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t *>(p) = w[0];
+}
+
+// Elements [c, c + 16) of the row at `row`; those at n and behind are 0.  VEC:
+// bytes that the row's address and every 16-element piece of it allow (32, 16,
+// 8, 4, or 0: single elements).
 template <int DT, int VEC>
 __device__ __forceinline__ void load16(const void *row, int64_t c, int64_t n, Raw16<DT> &r)
 {
     constexpr int SZ = dtype_size(DT), NV = SZ;             // 16-byte pieces
+    constexpr int PV = VEC == 32 ? 16 : VEC < SZ ? 0 : VEC; // bytes a piece of a chunk that ends inside
     const uint8_t *p = static_cast<const uint8_t *>(row) + c * SZ;
     if (VEC == 32 && c + 16 <= n) {
 #pragma unroll
         for (int i = 0; i < NV; i += 2) load32(p + 16 * i, r.v[i], r.v[i + 1]);
-    } else if (VEC == 16 && c + 16 <= n) {
+        return;
+    }
+    uint32_t w[4 * NV];
+    auto elements = [&](int i) {                            // word i from single elements
+        if constexpr (SZ == 4) {
+            w[i] = c + i < n ? __ldg(reinterpret_cast<const uint32_t *>(p) + i) : 0u;
+        } else {
+            const uint32_t lo = c + 2 * i < n ? __ldg(reinterpret_cast<const uint16_t *>(p) + 2 * i) : 0u;
+            const uint32_t hi = c + 2 * i + 1 < n ? __ldg(reinterpret_cast<const uint16_t *>(p) + 2 * i + 1) : 0u;
+            w[i] = lo | (hi << 16);
+        }
+    };
+    if constexpr (PV >= 4) {
+        constexpr int WP = PV / 4, EP = PV / SZ;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) r.v[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
-    } else {
-        uint32_t w[4 * NV];
-#pragma unroll
-        for (int i = 0; i < 4 * NV; ++i) {
-            if constexpr (SZ == 4) {
-                w[i] = c + i < n ? __ldg(reinterpret_cast<const uint32_t *>(p) + i) : 0u;
+        for (int i = 0; i < 4 * NV; i += WP) {
+            if (c + (i / WP + 1) * EP <= n) {
+                load_words<PV>(p + 4 * i, w + i);
             } else {
-                const uint32_t lo = c + 2 * i < n ? __ldg(reinterpret_cast<const uint16_t *>(p) + 2 * i) : 0u;
-                const uint32_t hi = c + 2 * i + 1 < n ? __ldg(reinterpret_cast<const uint16_t *>(p) + 2 * i + 1) : 0u;
-                w[i] = lo | (hi << 16);
+#pragma unroll
+                for (int j = 0; j < WP; ++j) elements(i + j);
             }
         }
+    } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) r.v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        for (int i = 0; i < 4 * NV; ++i) elements(i);
     }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) r.v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
-// load16 with the width known at run time only (the same for the whole warp)
-template <int DT>
+// load16 with VEC 32 or 16 known at compile time, or a narrower width `vec`
+// known at run time only (VEC = 0)
+template <int DT, int VEC>
 __device__ __forceinline__ void load16_rt(int vec, const void *row, int64_t c, int64_t n, Raw16<DT> &r)
 {
-    if (vec == 32) load16<DT, 32>(row, c, n, r);
-    else if (vec == 16) load16<DT, 16>(row, c, n, r);
+    if constexpr (VEC != 0) load16<DT, VEC>(row, c, n, r);
+    else if (vec == 8) load16<DT, 8>(row, c, n, r);
+    else if (vec == 4) load16<DT, 4>(row, c, n, r);
     else load16<DT, 0>(row, c, n, r);
 }
 
@@ -212,29 +255,45 @@ __device__ __forceinline__ void store16(void *row, int64_t c, int64_t n, const f
             w[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
     }
-    auto piece = [&](int i) { return make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]); };
+    constexpr int PV = VEC == 32 ? 16 : VEC < SZ ? 0 : VEC;
     if (VEC == 32 && c + 16 <= n) {
 #pragma unroll
-        for (int i = 0; i < NV; i += 2) store32(p + 16 * i, piece(i), piece(i + 1));
-    } else if (VEC == 16 && c + 16 <= n) {
+        for (int i = 0; i < NV; i += 2)
+            store32(p + 16 * i, make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]),
+                    make_uint4(w[4 * i + 4], w[4 * i + 5], w[4 * i + 6], w[4 * i + 7]));
+        return;
+    }
+    auto elements = [&](int i) {                            // word i as single elements
+        if constexpr (SZ == 4) {
+            if (c + i < n) reinterpret_cast<uint32_t *>(p)[i] = w[i];
+        } else {
+            if (c + 2 * i < n) reinterpret_cast<uint16_t *>(p)[2 * i] = static_cast<uint16_t>(w[i]);
+            if (c + 2 * i + 1 < n) reinterpret_cast<uint16_t *>(p)[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
+        }
+    };
+    if constexpr (PV >= 4) {
+        constexpr int WP = PV / 4, EP = PV / SZ;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) reinterpret_cast<uint4 *>(p)[i] = piece(i);
-    } else {
+        for (int i = 0; i < 4 * NV; i += WP) {
+            if (c + (i / WP + 1) * EP <= n) {
+                store_words<PV>(p + 4 * i, w + i);
+            } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            if (c + i < n) {
-                if constexpr (SZ == 4) reinterpret_cast<uint32_t *>(p)[i] = w[i];
-                else reinterpret_cast<uint16_t *>(p)[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+                for (int j = 0; j < WP; ++j) elements(i + j);
             }
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4 * NV; ++i) elements(i);
     }
 }
 
-template <int DT>
+template <int DT, int VEC>
 __device__ __forceinline__ void store16_rt(int vec, void *row, int64_t c, int64_t n, const float (&f)[16])
 {
-    if (vec == 32) store16<DT, 32>(row, c, n, f);
-    else if (vec == 16) store16<DT, 16>(row, c, n, f);
+    if constexpr (VEC != 0) store16<DT, VEC>(row, c, n, f);
+    else if (vec == 8) store16<DT, 8>(row, c, n, f);
+    else if (vec == 4) store16<DT, 4>(row, c, n, f);
     else store16<DT, 0>(row, c, n, f);
 }
 

@@ -13,9 +13,13 @@
 // ceil(D / 32)), the padding holding zero codes, so that every row starts on
 // 16 bytes; scales fp32 [slots][H], MXFP4 bytes [slots][H][ceil(D / 32)].
 //
-// Both kernels move bytes: a lane owns 16 elements (a 32-byte load of a
+// Both kernels move bytes: a lane owns 16 elements (a 32-byte access of a
 // 16-bit type), a power of two of lanes a row, so that a row's maximum is a
-// few shuffles and a warp covers 32 / lanes heads of one token.
+// few shuffles and a warp covers 32 / lanes heads of one token.  8 heads of 128
+// bf16: 10.3 k tokens written as E4M3 in 13.3 us (64 MB, 4.8 TB/s) and read
+// back in 13.3; contexts of 75 k tokens read back from MXFP4 in 69.8 us (400
+// MB, 5.7 TB/s of 6.57 copied), from INT8 in 87.  A decode step's 64 tokens
+// take 1.6 and 2.6 us: launches and chains of loads.
 #pragma once
 
 #include "common.cuh"
@@ -50,9 +54,9 @@ struct WriteArgs {
 
 // NCH: chunks of 16 elements a lane (2 only for D > 512); TOK: tokens a warp,
 // all their loads in flight before the first is computed.
-constexpr int TOKENS = 4;
+constexpr int TOKENS = 2;
 
-template <int DT, int FMT, int NCH, int TOK>
+template <int DT, int FMT, int VEC, int NCH, int TOK>
 __global__ void __launch_bounds__(WARPS * 32) k_kv_write(const WriteArgs a)
 {
     constexpr int SZ = dtype_size(DT);
@@ -64,30 +68,25 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv_write(const WriteArgs a)
     const int h = (is_v ? rest - a.groups : rest) * (32 >> a.lph_log2) + (lane >> a.lph_log2);
     const int rb = row_bytes(FMT, a.D), sb = scale_bytes(FMT, a.D);
     pdl_wait();
+    // the loads do not wait for the slots: a skipped token's row is read all the same
+    fp4::Raw16<DT> raw[TOK][NCH];
     int64_t slot[TOK];
 #pragma unroll
     for (int k = 0; k < TOK; ++k) {
         const int64_t t = tb * TOK + k;
+        const bool in = t < a.T && h < a.H;
         slot[k] = t < a.T ? __ldg(a.slots + t) : -1;
-    }
-    fp4::Raw16<DT> raw[TOK][NCH];
-#pragma unroll
-    for (int k = 0; k < TOK; ++k) {
-        if (slot[k] >= a.num_slots) {
-            if (lane == 0) bad_index();
-            slot[k] = -1;
-        }
         const void *src = static_cast<const uint8_t *>(is_v ? a.v : a.k) +
-                          ((tb * TOK + k) * (is_v ? a.v_ld : a.k_ld) + static_cast<int64_t>(h) * a.D) * SZ;
+                          (t * (is_v ? a.v_ld : a.k_ld) + static_cast<int64_t>(h) * a.D) * SZ;
 #pragma unroll
-        for (int i = 0; i < NCH; ++i)
-            fp4::load16_rt<DT>(a.vec, src, (i * lph + sub) * 16, slot[k] >= 0 && h < a.H ? a.D : 0, raw[k][i]);
+        for (int i = 0; i < NCH; ++i) fp4::load16_rt<DT, VEC>(a.vec, src, (i * lph + sub) * 16, in ? a.D : 0, raw[k][i]);
     }
     uint8_t *const cache = is_v ? a.vc : a.kc;
     void *const scale = is_v ? a.vs : a.ks;
 #pragma unroll
     for (int k = 0; k < TOK; ++k) {
-        const bool live = slot[k] >= 0 && h < a.H;
+        if (slot[k] >= a.num_slots && lane == 0) bad_index();
+        const bool live = slot[k] >= 0 && slot[k] < a.num_slots && h < a.H;
         const int64_t row = slot[k] * a.H + h;
         float f[NCH][16];
         float m = 0.0f;
@@ -152,6 +151,8 @@ struct ReadArgs {
     void *k, *v;                       // [total, H, D]
     int B, H, D, groups, page_size;
     int lph_log2, vec;
+    int part_log2;                     // warps a token (a power of two)
+    uint64_t page_inv;                 // ceil(2^63 / page_size): positions are divided by a product
 };
 
 // Largest b in [0, B) with cu[b] <= t (-1 when t lies behind cu[B] or before
@@ -175,106 +176,100 @@ __device__ __forceinline__ int sequence_of(const int32_t *cu, int B, int64_t t, 
     return lo < B ? lo : -1;
 }
 
-template <int DT, int FMT, int NCH, int TOK>
-__global__ void __launch_bounds__(WARPS * 32) k_kv_read(const ReadArgs a)
+// 16 codes of a row and their scale
+template <int FMT>
+__device__ __forceinline__ void load_codes(const uint8_t *cache, const void *scale, int64_t row, int rb, int sb, int c,
+                                           uint4 &q, uint32_t &sc)
 {
-    constexpr int SZ = dtype_size(DT);
-    const int lane = threadIdx.x & 31, lph = 1 << a.lph_log2, sub = lane & (lph - 1);
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
-    const int64_t t0 = unit / a.groups * TOK;
-    const int h = static_cast<int>(unit % a.groups) * (32 >> a.lph_log2) + (lane >> a.lph_log2);
-    const int rb = row_bytes(FMT, a.D), sb = scale_bytes(FMT, a.D);
-    pdl_wait();
-    // the sequence of the first token; the others follow it or start a later one
-    int64_t row[TOK];                  // row of the cache, -1: zeros, -2: the output row is left as it was
-    int b = -1;
-    int64_t first = 0, end = 0, start = 0;                 // of sequence b
-    const int64_t total = min(a.total, static_cast<int64_t>(__ldg(a.cu + a.B)));
-#pragma unroll
-    for (int k = 0; k < TOK; ++k) {
-        const int64_t t = t0 + k;
-        row[k] = -2;
-        if (t >= total) continue;                          // the same for the whole warp
-        if (b < 0 || t >= end) {
-            b = sequence_of(a.cu, a.B, t, lane);
-            if (b < 0) continue;
-            first = __ldg(a.cu + b);
-            end = __ldg(a.cu + b + 1);
-            start = a.starts != nullptr ? __ldg(a.starts + b) : 0;
-        }
-        const int64_t pos = t - first + start;
-        const int64_t pi = pos / a.page_size;
-        const int64_t page = pos >= 0 && pi < a.max_pages ? __ldg(a.table + b * a.max_pages + pi) : -1;
-        if (page >= 0 && page < a.num_pages) {
-            row[k] = (page * a.page_size + (pos - pi * a.page_size)) * a.H + h;
-        } else {
-            row[k] = -1;
-            if (lane == 0) bad_index();
-        }
+    if constexpr (FMT == KV_MXFP4) {
+        const uint2 t = __ldg(reinterpret_cast<const uint2 *>(cache + row * rb + (c >> 1)));
+        q.x = t.x;
+        q.y = t.y;
+        sc = __ldg(static_cast<const uint8_t *>(scale) + row * sb + c / 32);
+    } else {
+        q = __ldg(reinterpret_cast<const uint4 *>(cache + row * rb + c));
+        sc = __ldg(static_cast<const uint32_t *>(scale) + row);
     }
-    if (h < a.H) {
+}
+
+template <int FMT>
+__device__ __forceinline__ void widen_codes(const uint4 &q, uint32_t scale, float (&f)[16])
+{
+    const float sc = FMT == KV_MXFP4 ? fp4::e8m0_value(scale) : __uint_as_float(scale);
+    if constexpr (FMT == KV_MXFP4) {
+        fp4::e2m1x8_decode(q.x, f);
+        fp4::e2m1x8_decode(q.y, f + 8);
+    } else {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            const int c = (i * lph + sub) * 16;
-            if (c >= a.D) break;
-            uint4 q[TOK][2];
-            float sc[TOK][2];
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (FMT == KV_INT8) {
+                // 2^23 + (code + 128) has the code's byte in its low bits
+                const uint32_t u = w[j] ^ 0x80808080u;
 #pragma unroll
-            for (int k = 0; k < TOK; ++k) {
+                for (int e = 0; e < 4; ++e)
+                    f[4 * j + e] = __fsub_rn(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + e)), 8388736.0f);
+            } else {
+                uint32_t h2[2];
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2[0]) : "h"(static_cast<uint16_t>(w[j])));
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2[1]) : "h"(static_cast<uint16_t>(w[j] >> 16)));
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const uint8_t *cache = n ? a.vc : a.kc;
-                    const void *scale = n ? a.vs : a.ks;
-                    q[k][n] = make_uint4(0u, 0u, 0u, 0u);
-                    sc[k][n] = 0.0f;
-                    if (row[k] >= 0) {
-                        if constexpr (FMT == KV_MXFP4) {
-                            const uint2 t2 = __ldg(reinterpret_cast<const uint2 *>(cache + row[k] * rb + (c >> 1)));
-                            q[k][n].x = t2.x;
-                            q[k][n].y = t2.y;
-                            sc[k][n] = fp4::e8m0_value(__ldg(static_cast<const uint8_t *>(scale) + row[k] * sb + c / 32));
-                        } else {
-                            q[k][n] = __ldg(reinterpret_cast<const uint4 *>(cache + row[k] * rb + c));
-                            sc[k][n] = __ldg(static_cast<const float *>(scale) + row[k]);
-                        }
-                    }
+                for (int e = 0; e < 2; ++e) {
+                    const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&h2[e]));
+                    f[4 * j + 2 * e] = p.x;
+                    f[4 * j + 2 * e + 1] = p.y;
                 }
             }
+        }
+    }
 #pragma unroll
-            for (int k = 0; k < TOK; ++k) {
-                if (row[k] == -2) continue;
+    for (int j = 0; j < 16; ++j) f[j] = __fmul_rn(f[j], sc);
+}
+
+// A warp (of 2^part_log2) reads one output row: it finds where the row lies, a
+// chain of dependent loads, and streams its heads with U groups of keys and
+// values in flight.
+template <int DT, int FMT, int VEC>
+__global__ void __launch_bounds__(WARPS * 32) k_kv_read(const ReadArgs a)
+{
+    constexpr int SZ = dtype_size(DT), U = 2;
+    const int lane = threadIdx.x & 31, lph = 1 << a.lph_log2, sub = lane & (lph - 1);
+    const int rb = row_bytes(FMT, a.D), sb = scale_bytes(FMT, a.D);
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
+    const int64_t t = unit >> a.part_log2;
+    const int part = static_cast<int>(unit & ((1 << a.part_log2) - 1));
+    pdl_wait();
+    const int b = t < a.total ? sequence_of(a.cu, a.B, t, lane) : -1;
+    if (b >= 0) {
+        const int64_t pos = t - __ldg(a.cu + b) + (a.starts != nullptr ? __ldg(a.starts + b) : 0);
+        // 0 <= pos < 2^32 and page_size < 2^31: the error of the quotient, pos / 2^63, is below 1 / page_size
+        const int64_t pi = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(pos) << 1, a.page_inv));
+        const int64_t page = pos >= 0 && pi < a.max_pages ? __ldg(a.table + b * a.max_pages + pi) : -1;
+        const bool ok = page >= 0 && page < a.num_pages;
+        if (!ok && lane == 0) bad_index();
+        const int64_t row0 = (page * a.page_size + (pos - pi * a.page_size)) * a.H, out0 = t * a.H;
+        for (int g = part; g < a.groups; g += U << a.part_log2) {
+            for (int c = sub * 16; c < a.D; c += lph * 16) {             // more than once for D > 512 only
+                uint4 q[U][2] = {};
+                uint32_t sc[U][2] = {};
+                int h[U];
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    float f[16];
-                    if constexpr (FMT == KV_MXFP4) {
-                        fp4::e2m1x8_decode(q[k][n].x, f);
-                        fp4::e2m1x8_decode(q[k][n].y, f + 8);
-                    } else {
-                        const uint32_t w[4] = {q[k][n].x, q[k][n].y, q[k][n].z, q[k][n].w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if constexpr (FMT == KV_INT8) {
-                                // 2^23 + (code + 128) has the code's byte in its low bits
-                                const uint32_t u = w[j] ^ 0x80808080u;
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    f[4 * j + e] = __fsub_rn(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + e)), 8388736.0f);
-                            } else {
-                                uint32_t h2[2];
-                                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2[0]) : "h"(static_cast<uint16_t>(w[j])));
-                                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2[1]) : "h"(static_cast<uint16_t>(w[j] >> 16)));
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&h2[e]));
-                                    f[4 * j + 2 * e] = p.x;
-                                    f[4 * j + 2 * e + 1] = p.y;
-                                }
-                            }
-                        }
+                for (int u = 0; u < U; ++u) {
+                    h[u] = (g + (u << a.part_log2)) * (32 >> a.lph_log2) + (lane >> a.lph_log2);
+                    if (ok && h[u] < a.H) {
+                        load_codes<FMT>(a.kc, a.ks, row0 + h[u], rb, sb, c, q[u][0], sc[u][0]);
+                        load_codes<FMT>(a.vc, a.vs, row0 + h[u], rb, sb, c, q[u][1], sc[u][1]);
                     }
+                }
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) f[j] = __fmul_rn(f[j], sc[k][n]);
-                    fp4::store16_rt<DT>(a.vec, static_cast<uint8_t *>(n ? a.v : a.k) + ((t0 + k) * a.H + h) * a.D * SZ, c, a.D, f);
+                for (int u = 0; u < U; ++u) {
+                    if (h[u] >= a.H) continue;
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        float f[16];
+                        widen_codes<FMT>(q[u][n], sc[u][n], f);
+                        fp4::store16_rt<DT, VEC>(a.vec, static_cast<uint8_t *>(n ? a.v : a.k) + (out0 + h[u]) * a.D * SZ, c, a.D, f);
+                    }
                 }
             }
         }

@@ -30,12 +30,12 @@ namespace {
 
 inline bool valid_fmt(int f) { return f == SQ_MXFP4 || f == SQ_NVFP4; }
 
-// The widest load (32 or 16 bytes, 0: single elements) that every 16-element
-// piece of rows `ld_bytes` apart allows.
+// The widest access (32, 16, 8 or 4 bytes, 0: single 2-byte elements) that
+// every 16-element piece of rows `ld_bytes` apart allows.
 inline int vec_bytes(const void *p, int64_t ld_bytes)
 {
     const uint64_t a = reinterpret_cast<uint64_t>(p) | static_cast<uint64_t>(ld_bytes);
-    return (a & 31) == 0 ? 32 : (a & 15) == 0 ? 16 : 0;
+    return (a & 31) == 0 ? 32 : (a & 15) == 0 ? 16 : (a & 7) == 0 ? 8 : (a & 3) == 0 ? 4 : 0;
 }
 
 // two blocks of the quantiser fit an SM (one pass over the SMs), about two of
@@ -71,6 +71,7 @@ cudaError_t launch_quant_vec(const fp4::QuantArgs &a, int fmt, cudaStream_t st)
     const int vec = vec_bytes(a.x, a.ld * dtype_size(DT));
     if (vec == 32) return launch_quant_fmt<DT, 32>(a, fmt, st);
     if (vec == 16) return launch_quant_fmt<DT, 16>(a, fmt, st);
+    if (vec >= 4) return launch_quant_fmt<DT, 4>(a, fmt, st);
     return launch_quant_fmt<DT, 0>(a, fmt, st);
 }
 
@@ -106,6 +107,7 @@ cudaError_t launch_dequant_vec(const fp4::DequantArgs &a, int fmt, cudaStream_t 
     const int vec = vec_bytes(a.out, a.K * dtype_size(DT));
     if (vec == 32) return launch_dequant<DT, 32>(a, fmt, st);
     if (vec == 16) return launch_dequant<DT, 16>(a, fmt, st);
+    if (vec >= 4) return launch_dequant<DT, 4>(a, fmt, st);
     return launch_dequant<DT, 0>(a, fmt, st);
 }
 
@@ -298,28 +300,28 @@ inline int lanes_log2(int D)
     return l;
 }
 
-// Calls launch(type, format, chunks of 16 elements a lane, tokens a warp) with
-// all four as compile-time constants.
-template <typename F> cudaError_t kv_dispatch(int dt, int fmt, int D, bool many, F &&launch)
+
+
+// Calls launch(type, format, access width) with all three as compile-time
+// constants (width 0: narrower than 16 bytes).
+template <typename F> cudaError_t kv_dispatch(int dt, int fmt, int vec, F &&launch)
 {
-    auto tokens = [&](auto d, auto f) -> cudaError_t {
-        using std::integral_constant;
-        if (D > 512) return launch(d, f, integral_constant<int, 2>(), integral_constant<int, 1>());
-        if (many) return launch(d, f, integral_constant<int, 1>(), integral_constant<int, kv::TOKENS>());
-        return launch(d, f, integral_constant<int, 1>(), integral_constant<int, 1>());
+    auto width = [&](auto d, auto f) -> cudaError_t {
+        if (vec == 32) return launch(d, f, std::integral_constant<int, 32>());
+        if (vec == 16) return launch(d, f, std::integral_constant<int, 16>());
+        return launch(d, f, std::integral_constant<int, 0>());
     };
     auto format = [&](auto d) -> cudaError_t {
-        if (fmt == SQ_KV_INT8) return tokens(d, std::integral_constant<int, kv::KV_INT8>());
-        if (fmt == SQ_KV_FP8) return tokens(d, std::integral_constant<int, kv::KV_FP8>());
-        return tokens(d, std::integral_constant<int, kv::KV_MXFP4>());
+        if (fmt == SQ_KV_INT8) return width(d, std::integral_constant<int, kv::KV_INT8>());
+        if (fmt == SQ_KV_FP8) return width(d, std::integral_constant<int, kv::KV_FP8>());
+        return width(d, std::integral_constant<int, kv::KV_MXFP4>());
     };
     if (dt == SQ_F32) return format(std::integral_constant<int, DT_F32>());
     if (dt == SQ_F16) return format(std::integral_constant<int, DT_F16>());
     return format(std::integral_constant<int, DT_BF16>());
 }
 
-// Several tokens a warp once that leaves every SM its 64 warps
-inline bool many_tokens(int64_t warps) { return warps >= static_cast<int64_t>(kv::TOKENS) * 64 * sm_count(); }
+constexpr int KV_READ_WARPS = 16;
 
 sq_status check_kv(int fmt, int dt, int64_t H, int64_t D)
 {
@@ -447,11 +449,15 @@ sq_status sq_kv_cache_write(const void *k, const void *v, sq_dtype dt, int64_t T
     const int es = dtype_size(dt);
     a.vec = std::min(vec_bytes(k, (k_ld * es) | (D * es)), vec_bytes(v, (v_ld * es) | (D * es)));
     const cudaStream_t st = as_stream(stream);
-    const cudaError_t e = kv_dispatch(dt, fmt, a.D, many_tokens(T * 2 * a.groups), [&](auto d, auto f, auto nch, auto tok) {
-        constexpr int TOK = decltype(tok)::value;
-        const dim3 grid(static_cast<unsigned>(cdiv(cdiv(T, TOK) * 2 * a.groups, kv::WARPS)));
-        return launch_pdl(kv::k_kv_write<decltype(d)::value, decltype(f)::value, decltype(nch)::value, TOK>, grid,
-                          dim3(kv::WARPS * 32), 0, st, a);
+    // several tokens a warp once that leaves every SM its 64 warps
+    const bool many = T * 2 * a.groups >= static_cast<int64_t>(kv::TOKENS) * 64 * sm_count();
+    const cudaError_t e = kv_dispatch(dt, fmt, a.vec, [&](auto d, auto f, auto w) {
+        constexpr int DT = decltype(d)::value, FMT = decltype(f)::value, VEC = decltype(w)::value;
+        const int64_t tok = D <= 512 && many ? kv::TOKENS : 1;
+        const dim3 grid(static_cast<unsigned>(cdiv(cdiv(T, tok) * 2 * a.groups, kv::WARPS))), block(kv::WARPS * 32);
+        if (D > 512) return launch_pdl(kv::k_kv_write<DT, FMT, VEC, 2, 1>, grid, block, 0, st, a);
+        if (many) return launch_pdl(kv::k_kv_write<DT, FMT, VEC, 1, kv::TOKENS>, grid, block, 0, st, a);
+        return launch_pdl(kv::k_kv_write<DT, FMT, VEC, 1, 1>, grid, block, 0, st, a);
     });
     return e == cudaSuccess ? check_launch() : cuda_fail(e);
 }
@@ -482,16 +488,18 @@ sq_status sq_kv_cache_read(sq_kv_format fmt, const void *k_cache, const void *k_
     kv::ReadArgs a{static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), k_scale, v_scale,
                    num_pages, max_pages, table, cu_rows, starts, total, k_out, v_out, static_cast<int>(B),
                    static_cast<int>(H), static_cast<int>(D), static_cast<int>(cdiv(H, 32 >> ll)),
-                   static_cast<int>(page_size), ll, 0};
-    if (cdiv(total * a.groups, kv::WARPS) >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
+                   static_cast<int>(page_size), ll, 0, 0, 0};
     const int es = dtype_size(out_dt);
     a.vec = std::min(vec_bytes(k_out, D * es), vec_bytes(v_out, D * es));
     const cudaStream_t st = as_stream(stream);
-    const cudaError_t e = kv_dispatch(out_dt, fmt, a.D, many_tokens(total * a.groups), [&](auto d, auto f, auto nch, auto tok) {
-        constexpr int TOK = decltype(tok)::value;
-        const dim3 grid(static_cast<unsigned>(cdiv(cdiv(total, TOK) * a.groups, kv::WARPS)));
-        return launch_pdl(kv::k_kv_read<decltype(d)::value, decltype(f)::value, decltype(nch)::value, TOK>, grid,
-                          dim3(kv::WARPS * 32), 0, st, a);
+    // one warp a row, or more while the heads allow and the SMs are not full
+    while ((2 << a.part_log2) <= a.groups && (total << a.part_log2) < static_cast<int64_t>(KV_READ_WARPS) * sm_count()) ++a.part_log2;
+    a.page_inv = ((uint64_t(1) << 63) + static_cast<uint64_t>(page_size) - 1) / static_cast<uint64_t>(page_size);
+    const int64_t blocks = cdiv(total << a.part_log2, kv::WARPS);
+    if (blocks >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
+    const cudaError_t e = kv_dispatch(out_dt, fmt, a.vec, [&](auto d, auto f, auto w) {
+        return launch_pdl(kv::k_kv_read<decltype(d)::value, decltype(f)::value, decltype(w)::value>,
+                          dim3(static_cast<unsigned>(blocks)), dim3(kv::WARPS * 32), 0, st, a);
     });
     return e == cudaSuccess ? check_launch() : cuda_fail(e);
 }
