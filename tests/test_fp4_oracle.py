@@ -157,3 +157,14 @@ def test_sizes_of_what_cannot_be():
     assert [sq.kv_scale_bytes(f, 100) for f in range(3)] == [4, 4, 4] and sq.kv_scale_bytes(2, 128) == 4
     with pytest.raises(ValueError):
         sq.kv_row_bytes(sq.KV_INT8, 2000)
+
+
+@pytest.mark.parametrize("arg,error", [(None, TypeError), (3, TypeError), (torch.zeros(4, 64), ValueError)])
+def test_calls_take_cuda_tensors_only(arg, error):
+    u = torch.zeros(4, 32, dtype=torch.uint8)
+    for call in (lambda: sq.smooth_scales_nvfp4(arg, u, 0.5, u), lambda: sq.quant_weight_fp4(arg, None, sq.MXFP4, u, u),
+                 lambda: sq.smooth_quant_act_fp4(arg, None, sq.MXFP4, u, u), lambda: sq.dequant_fp4(u, u, sq.MXFP4, arg),
+                 lambda: sq.linear_fp4(u, u, u, u, sq.MXFP4, arg), lambda: sq.kv_cache_write(arg, arg, u, sq.KV_INT8, u, u, u, u),
+                 lambda: sq.kv_cache_read(sq.KV_INT8, u, u, u, u, u, u, arg, arg)):
+        with pytest.raises(error):
+            call()

@@ -132,6 +132,12 @@ def _load() -> ctypes.CDLL:
 
 _lib = _load()
 
+if not os.path.exists(os.path.join(_HERE, "_sqbind.so")):
+    raise ImportError(f"{_HERE}/_sqbind.so is missing: build it with `python w8a8_post_quantization_calib_b200/build.py`")
+from . import _sqbind  # noqa: E402  (links libsq.so, loaded above)
+
+_sqbind.set_error(SQError)
+
 
 def lib() -> ctypes.CDLL:
     return _lib
@@ -445,21 +451,8 @@ def linear_w8a8_f16scales(xq, wq, a_scale, mode: int, w_scale, y, bias=None, wor
 
 
 # ---------------------------------------------------------------- 4-bit microscaled formats
-def _on_current(*tensors) -> int:
-    """Index of the current device; every tensor given (None aside) has to be on it."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"every tensor must be on the current device cuda:{dev}, got one on {t.device}")
-    return dev
-
-
-def _raw_stream(stream, dev: int) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
+# The calls below are bound natively (csrc/bind.cpp): they take tensors on the current device, use its current stream
+# unless another is given, and raise TypeError, ValueError or SQError.
 def fp4_code_bytes(K: int) -> int:
     """Bytes of a row of K codes: 16 * ceil(K / 32)."""
     return (K + 31) // 32 * 16
@@ -473,36 +466,9 @@ def fp4_scale_bytes(fmt: int, rows: int, K: int) -> int:
     return n
 
 
-def _fp4_operand(q, sf, rows: int, K: int, fmt: int, name: str) -> None:
-    """Codes uint8 [rows, fp4_code_bytes(K)] and at least their scales' bytes."""
-    if q.dtype != torch.uint8 or sf.dtype != torch.uint8:
-        raise TypeError(f"{name} codes and scales must be torch.uint8")
-    if not (q.is_contiguous() and sf.is_contiguous()):
-        raise ValueError(f"{name} codes and scales must be contiguous")
-    if tuple(q.shape) != (rows, fp4_code_bytes(K)):
-        raise ValueError(f"{name} codes must be [{rows}, {fp4_code_bytes(K)}], got {tuple(q.shape)}")
-    if rows and sf.numel() < fp4_scale_bytes(fmt, rows, K):
-        raise ValueError(f"{name} scales must hold {fp4_scale_bytes(fmt, rows, K)} bytes, got {sf.numel()}")
-
-
-def _f32_vector(t, n: int, name: str):
-    """Pointer of an optional fp32 vector of n elements."""
-    if t is None:
-        return None
-    if t.dtype != torch.float32 or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous torch.float32 tensor")
-    if t.numel() != n:
-        raise ValueError(f"{name} must hold {n} elements, got {t.numel()}")
-    return t.data_ptr()
-
-
 def smooth_scales_nvfp4(act_max, w_max, alpha: float, s, g_act=None, g_w=None, stream=None) -> None:
     """smooth_scales with NVFP4's tensor scales of the smoothed activations and weight (fp32 [1] each, or None)."""
-    dev = _on_current(act_max, w_max, s, g_act, g_w)
-    K = act_max.numel()
-    _check("sq_smooth_scales_nvfp4", _lib.sq_smooth_scales_nvfp4(
-        _f32_vector(act_max, K, "act_max"), _f32_vector(w_max, K, "w_max"), K, float(alpha), _f32_vector(s, K, "s"),
-        _f32_vector(g_act, 1, "g_act"), _f32_vector(g_w, 1, "g_w"), _raw_stream(stream, dev)))
+    _sqbind.smooth_scales_nvfp4(act_max, w_max, alpha, s, g_act, g_w, stream)
 
 
 def quant_weight_fp4(w, s, fmt: int, wq4, w_sf, g=None, stream=None) -> None:
@@ -510,62 +476,22 @@ def quant_weight_fp4(w, s, fmt: int, wq4, w_sf, g=None, stream=None) -> None:
 
     s: fp32 [K] or None; g: NVFP4's tensor scale, fp32 [1] or None (1).
     """
-    dev = _on_current(w, s, wq4, w_sf, g)
-    N, K = w.shape
-    if not w.is_contiguous():
-        raise ValueError("w must be contiguous")
-    _fp4_operand(wq4, w_sf, N, K, fmt, "weight")
-    _check("sq_quant_weight_fp4", _lib.sq_quant_weight_fp4(
-        w.data_ptr(), _dt(w), N, K, _f32_vector(s, K, "s"), int(fmt), _f32_vector(g, 1, "g"), wq4.data_ptr(),
-        w_sf.data_ptr(), _raw_stream(stream, dev)))
+    _sqbind.quant_weight_fp4(w, s, fmt, wq4, w_sf, g, stream)
 
 
 def smooth_quant_act_fp4(x, s, fmt: int, xq4, x_sf, g=None, stream=None) -> None:
     """4-bit blocks of x * recip(s_j) for a 2-D x whose rows may lie in wider ones; arguments as quant_weight_fp4."""
-    dev = _on_current(x, s, xq4, x_sf, g)
-    M, K = x.shape
-    ld = x.stride(0)
-    if K > 1 and x.stride(1) != 1:
-        raise ValueError("x rows must be contiguous")
-    if M <= 1:
-        ld = max(ld, K)
-    elif ld < K:
-        raise ValueError("x rows must not overlap")
-    _fp4_operand(xq4, x_sf, M, K, fmt, "activation")
-    _check("sq_smooth_quant_act_fp4", _lib.sq_smooth_quant_act_fp4(
-        x.data_ptr(), _dt(x), M, K, ld, _f32_vector(s, K, "s"), int(fmt), _f32_vector(g, 1, "g"), xq4.data_ptr(),
-        x_sf.data_ptr(), _raw_stream(stream, dev)))
+    _sqbind.smooth_quant_act_fp4(x, s, fmt, xq4, x_sf, g, stream)
 
 
 def dequant_fp4(q4, sf, fmt: int, out, g=None, stream=None) -> None:
     """out [rows, K] = the values that the codes stand for, rounded to out's type."""
-    dev = _on_current(q4, sf, out, g)
-    rows, K = out.shape
-    if not out.is_contiguous():
-        raise ValueError("out must be contiguous")
-    _fp4_operand(q4, sf, rows, K, fmt, "the")
-    _check("sq_dequant_fp4", _lib.sq_dequant_fp4(
-        q4.data_ptr(), sf.data_ptr(), int(fmt), rows, K, _f32_vector(g, 1, "g"), _dt(out), out.data_ptr(),
-        _raw_stream(stream, dev)))
+    _sqbind.dequant_fp4(q4, sf, fmt, out, g, stream)
 
 
 def linear_fp4(xq4, x_sf, wq4, w_sf, fmt: int, y, bias=None, g_act=None, g_w=None, stream=None) -> None:
     """y [M, N] = packed activations times packed weight of one format (K: the codes' row length), plus bias."""
-    dev = _on_current(xq4, x_sf, wq4, w_sf, y, bias, g_act, g_w)
-    M, N = y.shape
-    K = 2 * wq4.shape[-1]
-    if not y.is_contiguous():
-        raise ValueError("y must be contiguous")
-    _fp4_operand(xq4, x_sf, M, K, fmt, "activation")
-    _fp4_operand(wq4, w_sf, N, K, fmt, "weight")
-    b = None
-    if bias is not None:
-        if bias.dtype != y.dtype or bias.numel() != N or not bias.is_contiguous():
-            raise ValueError(f"bias must be a contiguous {y.dtype} tensor of {N} elements")
-        b = bias.data_ptr()
-    _check("sq_linear_fp4", _lib.sq_linear_fp4(
-        xq4.data_ptr(), x_sf.data_ptr(), wq4.data_ptr(), w_sf.data_ptr(), int(fmt), M, N, K,
-        _f32_vector(g_act, 1, "g_act"), _f32_vector(g_w, 1, "g_w"), b, _dt(y), y.data_ptr(), _raw_stream(stream, dev)))
+    _sqbind.linear_fp4(xq4, x_sf, wq4, w_sf, fmt, y, bias, g_act, g_w, stream)
 
 
 # ---------------------------------------------------------------- quantised key/value cache
@@ -585,21 +511,6 @@ def kv_scale_bytes(fmt: int, D: int) -> int:
     return n
 
 
-def _kv_cache(fmt: int, H: int, D: int, k_cache, k_scale, v_cache, v_scale):
-    """Checks the four cache tensors; returns (pages, page size)."""
-    rb, sb = kv_row_bytes(fmt, D), kv_scale_bytes(fmt, D)
-    codes = torch.int8 if fmt == KV_INT8 else torch.uint8
-    P, S = k_cache.shape[0], k_cache.shape[1]
-    for c, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if c.dtype != codes or not c.is_contiguous() or tuple(c.shape) != (P, S, H, rb):
-            raise ValueError(f"{n} must be a contiguous {codes} tensor [{P}, {S}, {H}, {rb}], got {c.dtype} {tuple(c.shape)}")
-    want = (torch.uint8, (P, S, H, sb)) if fmt == KV_MXFP4 else (torch.float32, (P, S, H))
-    for c, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if c.dtype != want[0] or not c.is_contiguous() or tuple(c.shape) != want[1]:
-            raise ValueError(f"{n} must be a contiguous {want[0]} tensor {list(want[1])}, got {c.dtype} {tuple(c.shape)}")
-    return P, S
-
-
 def kv_cache_write(k, v, slots, fmt: int, k_cache, k_scale, v_cache, v_scale, stream=None) -> None:
     """Quantises keys and values [T, H, D] (a token's heads contiguous, tokens any stride apart) into their slots.
 
@@ -607,23 +518,7 @@ def kv_cache_write(k, v, slots, fmt: int, k_cache, k_scale, v_cache, v_scale, st
     KV_INT8, else uint8) [pages, page_size, H, kv_row_bytes], scales float32 [pages, page_size, H], or uint8
     [pages, page_size, H, ceil(D / 32)] for KV_MXFP4.  A slot behind the cache is not written; sync_status reports it.
     """
-    dev = _on_current(k, v, slots, k_cache, k_scale, v_cache, v_scale)
-    T, H, D = k.shape
-    if v.shape != k.shape or v.dtype != k.dtype:
-        raise ValueError("k and v must match")
-    lds = []
-    for x, n in ((k, "k"), (v, "v")):
-        if (D > 1 and x.stride(2) != 1) or (H > 1 and x.stride(1) != D):
-            raise ValueError(f"the heads of a token of {n} must be contiguous")
-        if T > 1 and x.stride(0) < H * D:
-            raise ValueError(f"the tokens of {n} must not overlap")
-        lds.append(x.stride(0) if T > 1 else H * D)
-    if slots.dtype != torch.int64 or tuple(slots.shape) != (T,) or not slots.is_contiguous():
-        raise ValueError(f"slots must be a contiguous torch.int64 tensor [{T}]")
-    P, S = _kv_cache(fmt, H, D, k_cache, k_scale, v_cache, v_scale)
-    _check("sq_kv_cache_write", _lib.sq_kv_cache_write(
-        k.data_ptr(), v.data_ptr(), _dt(k), T, H, D, lds[0], lds[1], slots.data_ptr(), int(fmt), P * S,
-        k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(), v_scale.data_ptr(), _raw_stream(stream, dev)))
+    _sqbind.kv_cache_write(k, v, slots, fmt, k_cache, k_scale, v_cache, v_scale, stream)
 
 
 def kv_cache_read(fmt: int, k_cache, k_scale, v_cache, v_scale, table, cu_rows, k_out, v_out, starts=None,
@@ -633,18 +528,4 @@ def kv_cache_read(fmt: int, k_cache, k_scale, v_cache, v_scale, table, cu_rows, 
     table: int32 [B, max_pages]; cu_rows: int32 [B + 1], sequence b's output rows are cu_rows[b] .. cu_rows[b + 1] - 1
     and hold its positions from starts[b] (int32 [B]; None: 0) on.  Rows outside are left as they were.
     """
-    dev = _on_current(k_cache, k_scale, v_cache, v_scale, table, cu_rows, k_out, v_out, starts)
-    total, H, D = k_out.shape
-    if v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
-        raise ValueError("k_out and v_out must match")
-    if not (k_out.is_contiguous() and v_out.is_contiguous()):
-        raise ValueError("k_out and v_out must be contiguous")
-    P, S = _kv_cache(fmt, H, D, k_cache, k_scale, v_cache, v_scale)
-    B, pages = table.shape
-    for x, shape, n in ((table, (B, pages), "table"), (cu_rows, (B + 1,), "cu_rows"), (starts, (B,), "starts")):
-        if x is not None and (x.dtype != torch.int32 or tuple(x.shape) != shape or not x.is_contiguous()):
-            raise ValueError(f"{n} must be a contiguous torch.int32 tensor {list(shape)}")
-    _check("sq_kv_cache_read", _lib.sq_kv_cache_read(
-        int(fmt), k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(), v_scale.data_ptr(), P, S, H, D,
-        table.data_ptr(), B, pages, cu_rows.data_ptr(), None if starts is None else starts.data_ptr(), total,
-        _dt(k_out), k_out.data_ptr(), v_out.data_ptr(), _raw_stream(stream, dev)))
+    _sqbind.kv_cache_read(fmt, k_cache, k_scale, v_cache, v_scale, table, cu_rows, k_out, v_out, starts, stream)

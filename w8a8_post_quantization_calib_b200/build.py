@@ -1,11 +1,14 @@
 """Build libsq.so (the CUDA kernels + C ABI) and libsq_peak.so (the tensor-core
 peak measurement used as the GEMM roofline denominator) in-tree with nvcc for
-sm_100a."""
+sm_100a, and _sqbind.so (libsq's calls for PyTorch tensors) with the host
+compiler against the installed torch."""
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +23,8 @@ OBJ = os.path.join(HERE, "_build")
 PEAK_SO = os.path.join(HERE, "libsq_peak.so")
 PEAK_SOURCES = ["peak.cu"]
 PEAK_HEADERS = ["common.cuh", "ptx_sm100.cuh"]
+BIND_SO = os.path.join(HERE, "_sqbind.so")
+BIND_SOURCES = ["bind.cpp"]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
@@ -46,6 +51,16 @@ def _stale(so: str, sources, headers) -> bool:
 
 def _nvcc_cmd(out: str, args, extra) -> list[str]:
     return [nvcc(), *NVCC_FLAGS, *(extra or []), "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-o", out, *args]
+
+
+def _bind_cmd(out: str) -> list[str]:
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    includes = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
+                os.path.join(cuda, "include")]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", *[f"-I{d}" for d in includes], "-o", out,
+            *[os.path.join(CSRC, f) for f in BIND_SOURCES], "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda",
+            "-ltorch_cpu", "-ltorch_python", "-L" + HERE, "-l:libsq.so", "-Wl,-rpath,$ORIGIN"]
 
 
 def _run(jobs, verbose: bool) -> None:
@@ -84,6 +99,8 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     objs = [os.path.join(OBJ, unit[:-3] + ".o") for unit in UNITS]
     if force or not os.path.exists(SO) or any(os.path.getmtime(o) > os.path.getmtime(SO) for o in objs):
         _run([job(SO, ["-shared", *objs], None)], verbose)
+    if force or _stale(BIND_SO, BIND_SOURCES, []):
+        _run([(BIND_SO + tag, BIND_SO, _bind_cmd(BIND_SO + tag))], verbose)
     return SO
 
 

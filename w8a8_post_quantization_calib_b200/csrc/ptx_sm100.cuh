@@ -21,14 +21,6 @@ __device__ __forceinline__ uint64_t global_timer_ns()
     return t;
 }
 
-// True in one lane of a converged warp, the same one at every call.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
 {
@@ -337,31 +329,6 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-
-// Arrive on a barrier of any CTA of the cluster without publishing writes to
-// memory: for work in tensor memory (reads or writes that tcgen05.wait has
-// seen complete, ordered by the tcgen05 fences around the barrier) and for
-// buffers that asynchronous operations have finished with.  mbar_arrive_cluster
-// publishes this thread's writes at cluster scope, which takes ~0.8 us.
-__device__ __forceinline__ void mbar_arrive_plain(uint32_t cluster_bar)
-{
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-
-// 16-byte store to shared memory of a CTA of this cluster, counted as 16
-// transaction bytes on that CTA's barrier (both addresses from mapa).
-__device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t bar, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
-{
-    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(addr),
-                 "r"(bar), "r"(a), "r"(b), "r"(c), "r"(d)
-                 : "memory");
-}
-
-// All threads of the cluster meet; no memory is published.
-__device__ __forceinline__ void cluster_meet()
-{
-    asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 
 // try_wait with cluster-scope acquire: writes that CTAs of the cluster made
