@@ -549,8 +549,9 @@ sq_status sq_dequant_fp4(const uint8_t *q4, const uint8_t *sf, sq_fp4_format fmt
  * g_act, g_w: fp32 [1] or NULL (1), read for NVFP4 only.  bias: [N] of out_dt
  * or NULL.  y: [M, N] of out_dt, contiguous, any N >= 1 (rows of a multiple
  * of 16 bytes at a 16-byte aligned y take the fast stores).  M = 0: no-op.
- * No workspace: M <= 128 streams the weight, a cluster of CTAs sharing a
- * tile's K range where the tiles are few; M > 128 runs CTA pairs. */
+ * No workspace: up to M = 128, and above where tiles are few and K is long, a
+ * cluster of CTAs shares a tile's K range; else CTA pairs.  Repeated calls give
+ * the same bits. */
 sq_status sq_linear_fp4(const uint8_t *xq4, const uint8_t *x_sf, const uint8_t *wq4, const uint8_t *w_sf,
                         sq_fp4_format fmt, int64_t M, int64_t N, int64_t K, const float *g_act, const float *g_w,
                         const void *bias, sq_dtype out_dt, void *y, sq_stream stream);

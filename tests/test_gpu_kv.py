@@ -86,7 +86,7 @@ def test_write_and_read(H, D, fmt, dt):
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("S", [1, 16, 24])
-@pytest.mark.parametrize("H,D", [(5, 80), (8, 128)])
+@pytest.mark.parametrize("H,D", [(5, 80), (8, 128), (1, 64), (3, 31), (32, 100), (2, 512), (2, 600)])
 def test_ragged_spans(fmt, S, H, D):
     """Uneven sequences, an empty one in front, amid and last; spans that start and end inside a page; rows before
     the first sequence and behind the last stay."""

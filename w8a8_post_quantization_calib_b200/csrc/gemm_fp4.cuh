@@ -173,8 +173,9 @@ __device__ __forceinline__ float out_factor(const Fp4Params &fp)
 }
 
 // ---------------------------------------------------------------------------
-// Small M: A = weights [N, K], B = activations [M, K] (M <= 128, one token
-// tile); a TMEM lane is an output channel, a column a token.  A cluster of CS
+// Few tiles: A = weights [N, K], B = activations [M, K] in tiles of BN tokens
+// (more than one for BN = 128 only); a TMEM lane is an output channel, a column
+// a token.  A cluster of CS
 // CTAs shares a weight tile's K range; two CTAs fit an SM.  The partial sums
 // are reduced by the whole cluster: groups of four tokens are dealt out to the
 // CTAs in turn, and each is sent the others' sums of its own (st.async into its
@@ -250,7 +251,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 2)
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int rank = CS > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
-    const int groups = (p.M + 3) >> 2;                     // of four tokens
+    // token tiles of one weight tile's clusters are tiles_r clusters apart
+    const int cluster = static_cast<int>(blockIdx.x) / CS;
+    const int tc = cluster / p.tiles_r, tile = cluster - tc * p.tiles_r;
+    const int tokens = min(BN, p.M - tc * BN);             // of this tile
+    const int groups = (tokens + 3) >> 2;                  // of four tokens
     auto owned = [&](int r) { return (groups - r + CS - 1) / CS; };      // groups r, r + CS, ...
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -284,7 +289,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 2)
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const uint64_t tmo = p.timeout_ns;
     // this CTA's share of its tile's K blocks
-    const int tile = static_cast<int>(blockIdx.x) / CS;
     const int kb_begin = static_cast<int>(static_cast<int64_t>(rank) * p.num_kb / CS);
     const int kb_end = static_cast<int>(static_cast<int64_t>(rank + 1) * p.num_kb / CS);
     pdl_wait();                        // operands and scales come from the previous kernels
@@ -308,8 +312,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 2)
                 const uint32_t ssa = sb + C::B_BYTES, ssb = ssa + C::SF_BYTES;
                 ptx::tma_load_2d(sa, &map_w, fb, kb * BKB, tile * BM);
                 ptx::tma_load_3d(ssa, &map_ws, fb, 0, kb * Sf::TILES, tile);
-                ptx::tma_load_2d(sb, &map_x, fb, kb * BKB, 0);
-                ptx::tma_load_3d(ssb, &map_xs, fb, 0, kb * Sf::TILES, 0);
+                ptx::tma_load_2d(sb, &map_x, fb, kb * BKB, tc * BN);
+                ptx::tma_load_3d(ssb, &map_xs, fb, 0, kb * Sf::TILES, tc);
             }
             __syncwarp();
             ++issued;
@@ -399,7 +403,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 2)
         auto emit = [&](auto dt) {
             constexpr int DT = decltype(dt)::value;
             constexpr int SZ = dtype_size(DT);
-            uint8_t *out = static_cast<uint8_t *>(p.out) + (static_cast<int64_t>(rank) * 4 * p.N + n) * SZ;
+            uint8_t *out = static_cast<uint8_t *>(p.out) + ((static_cast<int64_t>(tc) * BN + rank * 4) * p.N + n) * SZ;
             const int64_t token = static_cast<int64_t>(p.N) * SZ;
 #pragma unroll 1
             for (int j = 0; j < mine; j += 4) {
@@ -425,7 +429,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 2)
                             acc[2] += o.z;
                             acc[3] += o.w;
                         }
-                        const int left = n < p.N ? p.M - ((j + i) * CS + rank) * 4 : 0;
+                        const int left = n < p.N ? tokens - ((j + i) * CS + rank) * 4 : 0;
                         if (left >= 4) {
 #pragma unroll
                             for (int t = 0; t < 4; ++t) gemm::store_out(out + t * token, DT, 0, __fmaf_rn(acc[t], factor, bn));

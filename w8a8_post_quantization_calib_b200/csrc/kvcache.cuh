@@ -152,7 +152,8 @@ struct ReadArgs {
     int B, H, D, groups, page_size;
     int lph_log2, vec;
     int part_log2;                     // warps a token (a power of two)
-    uint64_t page_inv;                 // ceil(2^63 / page_size): positions are divided by a product
+    uint64_t page_inv, head_inv;       // ceil(2^63 / page_size), ceil(2^63 / H): division by a product
+    int lanes;                         // k_kv_read_rows: lanes a row
 };
 
 // Largest b in [0, B) with cu[b] <= t (-1 when t lies behind cu[B] or before
@@ -271,6 +272,83 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv_read(const ReadArgs a)
                         fp4::store16_rt<DT, VEC>(a.vec, static_cast<uint8_t *>(n ? a.v : a.k) + (out0 + h[u]) * a.D * SZ, c, a.D, f);
                     }
                 }
+            }
+        }
+    }
+    __syncthreads();
+    pdl_trigger();
+}
+
+// Rows whose lanes are no power of two, or fewer heads than a warp has rows:
+// output rows (token, head) laid end to end, 32 / lanes of them a step, U steps
+// a warp.  Every lane finds its own row's place, starting from the sequence of
+// the warp's first token.  D <= 512.
+template <int DT, int FMT, int VEC>
+__global__ void __launch_bounds__(WARPS * 32) k_kv_read_rows(const ReadArgs a)
+{
+    constexpr int SZ = dtype_size(DT), U = 2;
+    const int lane = threadIdx.x & 31;
+    const int per = 32 / a.lanes, j = lane / a.lanes, c = (lane - j * a.lanes) * 16;
+    const int rb = row_bytes(FMT, a.D), sb = scale_bytes(FMT, a.D);
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
+    const int64_t r0 = unit * (U * per), rows = a.total * a.H;
+    // r < 2^47 and H <= 2^16: the error of the quotient, r / 2^63, is below 1 / H
+    auto token = [&](int64_t r) { return static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(r) << 1, a.head_inv)); };
+    pdl_wait();
+    if (r0 < rows) {
+        const int b0 = max(sequence_of(a.cu, a.B, token(r0), lane), 0);
+        const int64_t first0 = __ldg(a.cu + b0), end0 = __ldg(a.cu + b0 + 1);
+        const int64_t start0 = a.starts != nullptr ? __ldg(a.starts + b0) : 0;
+        int64_t row[U];                // row of the cache, -1: outside (zeros), -2: the output row stays
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = r0 + u * per + j, t = token(r);
+            row[u] = -2;
+            if (j >= per || r >= rows) continue;
+            int b = b0;
+            int64_t first = first0, end = end0, start = start0;
+            if (t >= end && b + 1 < a.B) {
+                int step = 1;                               // the answer lies before b + step
+                while (b + step < a.B && __ldg(a.cu + b + step) <= t) {
+                    b += step;
+                    step = min(2 * step, a.B);
+                }
+                while (step > 1) {
+                    step = (step + 1) / 2;
+                    if (b + step < a.B && __ldg(a.cu + b + step) <= t) b += step;
+                }
+                first = __ldg(a.cu + b);
+                end = __ldg(a.cu + b + 1);
+                start = a.starts != nullptr ? __ldg(a.starts + b) : 0;
+            }
+            if (t < first || t >= end) continue;
+            const int64_t pos = t - first + start;
+            const int64_t pi = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(pos) << 1, a.page_inv));
+            const int64_t page = pos >= 0 && pi < a.max_pages ? __ldg(a.table + b * a.max_pages + pi) : -1;
+            if (page >= 0 && page < a.num_pages) {
+                row[u] = (page * a.page_size + (pos - pi * a.page_size)) * a.H + (r - t * a.H);
+            } else {
+                row[u] = -1;
+                bad_index();
+            }
+        }
+        uint4 q[U][2] = {};
+        uint32_t sc[U][2] = {};
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (row[u] >= 0) {
+                load_codes<FMT>(a.kc, a.ks, row[u], rb, sb, c, q[u][0], sc[u][0]);
+                load_codes<FMT>(a.vc, a.vs, row[u], rb, sb, c, q[u][1], sc[u][1]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (row[u] == -2) continue;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                float f[16];
+                widen_codes<FMT>(q[u][n], sc[u][n], f);
+                fp4::store16_rt<DT, VEC>(a.vec, static_cast<uint8_t *>(n ? a.v : a.k) + (r0 + u * per + j) * a.D * SZ, c, a.D, f);
             }
         }
     }

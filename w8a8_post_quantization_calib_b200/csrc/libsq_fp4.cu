@@ -160,7 +160,7 @@ sq_status launch_fp4_swap(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_t 
     if (!make_map(&mx, o.xq, false, o.row_bytes, fp.p.M, BN)) return SQ_ERR_CUDA;
     if (!make_scale_map(&mws, o.ws, o.ktiles, fp.p.N, KT, 1)) return SQ_ERR_CUDA;
     if (!make_scale_map(&mxs, o.xs, o.ktiles, fp.p.M, KT, 1)) return SQ_ERR_CUDA;
-    const dim3 grid(static_cast<unsigned>(fp.p.tiles_r * CS));
+    const dim3 grid(static_cast<unsigned>(fp.p.tiles_r * fp.p.tiles_c * CS));
     const int per_sm = static_cast<int64_t>(grid.x) <= sm_count() ? 1 : 2;
     const int smem = C::smem_bytes(per_sm);
     fp.p.ring = C::stages(per_sm);
@@ -183,22 +183,40 @@ sq_status launch_fp4_swap_cs(const fp4::Fp4Params &fp, const Fp4Operands &o, int
     return launch_fp4_swap<BN, 1, FMT>(fp, o, st);
 }
 
+// The largest cluster that leaves one CTA an SM and two K blocks a CTA: a
+// second CTA an SM only adds partial sums (M = 128, N = 4096, K = 4096: 10.2 /
+// 8.2 / 7.2 / 10.0 us with clusters of 1 / 2 / 4 / 8; M = 1, N = 11008: 6.4 with
+// 1, 7.0 with 2; M = 1, N = 512, K = 512: 2.7 with 1, 3.3 with 2), as from about
+// 90 CTAs on the weights come at HBM's rate.  Clusters of 8 only while they fill
+// two thirds of the SMs: 16 of them do not fit the GPCs at once (M = 512, N =
+// 512, K = 4096: 11.7 us with 16 clusters of 8).
+inline int swap_cluster(int64_t tiles, int64_t num_kb)
+{
+    int cs = 1;
+    if (!(g_inject & 2))
+        while (cs < 8 && 4 * cs <= num_kb && tiles * 2 * cs <= (cs == 4 ? 2 * sm_count() / 3 : sm_count())) cs *= 2;
+    return cs;
+}
+
+// Whether few tiles and a long K make the cluster split over K faster than CTA
+// pairs for M > 128: M = 256, N = 512, K = 4096 6.1 us (pairs 8.9), K = 2048 5.9
+// (6.9), K = 512 5.4 (5.4); M = 256, N = 4096, K = 4096 8.3 (9.5), K = 1024 6.4 (6.0).
+inline bool swap_for_long_k(int64_t M, int64_t N, int64_t num_kb)
+{
+    const int cs = swap_cluster(cdiv(N, gemm::BM) * cdiv(M, 128), num_kb);
+    return (cs >= 4 && num_kb >= 8) || (cs == 2 && num_kb >= 16);
+}
+
 template <int FMT>
 sq_status dispatch_fp4_swap(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_t st)
 {
     gemm::Params &p = fp.p;
     p.tiles_r = static_cast<int>(cdiv(p.N, gemm::BM));
+    p.tiles_c = static_cast<int>(cdiv(p.M, 128));
     p.num_kb = static_cast<int>(cdiv(o.row_bytes, 128));
     p.timeout_ns = g_timeout_ns;
     p.inject = g_inject & 1;
-    // the largest cluster that leaves one CTA an SM and two K blocks a CTA: a
-    // second CTA an SM only adds partial sums (M = 128, N = 4096, K = 4096:
-    // 10.2 / 8.2 / 7.2 / 10.0 us with clusters of 1 / 2 / 4 / 8; M = 1, N =
-    // 11008: 6.4 with 1, 7.0 with 2; M = 1, N = 512, K = 512: 2.7 with 1, 3.3
-    // with 2), as from about 90 CTAs on the weights come at HBM's rate
-    int cs = 1;
-    if (!(g_inject & 2))
-        while (cs < 8 && 4 * cs <= p.num_kb && static_cast<int64_t>(p.tiles_r) * 2 * cs <= sm_count()) cs *= 2;
+    const int cs = swap_cluster(static_cast<int64_t>(p.tiles_r) * p.tiles_c, p.num_kb);
     if (p.M <= 16) return launch_fp4_swap_cs<16, FMT>(fp, o, cs, st);
     if (p.M <= 32) return launch_fp4_swap_cs<32, FMT>(fp, o, cs, st);
     if (p.M <= 64) return launch_fp4_swap_cs<64, FMT>(fp, o, cs, st);
@@ -408,7 +426,7 @@ sq_status sq_linear_fp4(const uint8_t *xq4, const uint8_t *x_sf, const uint8_t *
     fp.g_w = fmt == SQ_NVFP4 ? g_w : nullptr;
     const Fp4Operands o{xq4, x_sf, wq4, w_sf, fp4::code_row_bytes(K), fp4::scale_tiles_k(fmt, K)};
     const cudaStream_t st = as_stream(stream);
-    if (M <= 128)
+    if (M <= 128 || swap_for_long_k(M, N, cdiv(o.row_bytes, 128)))
         return fmt == SQ_MXFP4 ? dispatch_fp4_swap<fp4::FMT_MX>(fp, o, st) : dispatch_fp4_swap<fp4::FMT_NV>(fp, o, st);
     return fmt == SQ_MXFP4 ? dispatch_fp4_pair<fp4::FMT_MX>(fp, o, st) : dispatch_fp4_pair<fp4::FMT_NV>(fp, o, st);
 }
@@ -488,18 +506,29 @@ sq_status sq_kv_cache_read(sq_kv_format fmt, const void *k_cache, const void *k_
     kv::ReadArgs a{static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), k_scale, v_scale,
                    num_pages, max_pages, table, cu_rows, starts, total, k_out, v_out, static_cast<int>(B),
                    static_cast<int>(H), static_cast<int>(D), static_cast<int>(cdiv(H, 32 >> ll)),
-                   static_cast<int>(page_size), ll, 0, 0, 0};
+                   static_cast<int>(page_size), ll, 0, 0, 0, 0, static_cast<int>(cdiv(D, 16))};
     const int es = dtype_size(out_dt);
     a.vec = std::min(vec_bytes(k_out, D * es), vec_bytes(v_out, D * es));
     const cudaStream_t st = as_stream(stream);
-    // one warp a row, or more while the heads allow and the SMs are not full
-    while ((2 << a.part_log2) <= a.groups && (total << a.part_log2) < static_cast<int64_t>(KV_READ_WARPS) * sm_count()) ++a.part_log2;
-    a.page_inv = ((uint64_t(1) << 63) + static_cast<uint64_t>(page_size) - 1) / static_cast<uint64_t>(page_size);
-    const int64_t blocks = cdiv(total << a.part_log2, kv::WARPS);
+    auto inverse = [](int64_t d) { return ((uint64_t(1) << 63) + static_cast<uint64_t>(d) - 1) / static_cast<uint64_t>(d); };
+    a.page_inv = inverse(page_size);
+    a.head_inv = inverse(H);
+    // Rows end to end where a warp a token would leave lanes idle or have one
+    // group of heads in flight: 1 head of 64 414 -> 60 us (45 at the copy rate), 2
+    // of 128 107 -> 58, 5 of 128 59 -> 48; 8 of 128 stay a warp a token (69 us
+    // against 73 for 75 k tokens, 2.7 against 3.4 for 64).
+    const bool by_rows = D <= 512 && ((16 << ll) != D || H % (32 >> ll) != 0 || a.groups < 2);
+    // one warp a token, or more while the heads allow and the SMs are not full
+    while (!by_rows && (2 << a.part_log2) <= a.groups && (total << a.part_log2) < static_cast<int64_t>(KV_READ_WARPS) * sm_count())
+        ++a.part_log2;
+    const int64_t warps = by_rows ? cdiv(total * H, 2 * (32 / a.lanes)) : total << a.part_log2;
+    const int64_t blocks = cdiv(warps, kv::WARPS);
     if (blocks >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
     const cudaError_t e = kv_dispatch(out_dt, fmt, a.vec, [&](auto d, auto f, auto w) {
-        return launch_pdl(kv::k_kv_read<decltype(d)::value, decltype(f)::value, decltype(w)::value>,
-                          dim3(static_cast<unsigned>(blocks)), dim3(kv::WARPS * 32), 0, st, a);
+        constexpr int DT = decltype(d)::value, FMT = decltype(f)::value, VEC = decltype(w)::value;
+        const dim3 grid(static_cast<unsigned>(blocks)), block(kv::WARPS * 32);
+        if (by_rows) return launch_pdl(kv::k_kv_read_rows<DT, FMT, VEC>, grid, block, 0, st, a);
+        return launch_pdl(kv::k_kv_read<DT, FMT, VEC>, grid, block, 0, st, a);
     });
     return e == cudaSuccess ? check_launch() : cuda_fail(e);
 }
