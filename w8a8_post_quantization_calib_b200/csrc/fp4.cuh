@@ -297,6 +297,74 @@ __device__ __forceinline__ void store16_rt(int vec, void *row, int64_t c, int64_
     else store16<DT, 0>(row, c, n, f);
 }
 
+// Rows that allow accesses of 4 or 2 bytes only (PB): a warp takes the 512
+// columns of its strip in pieces 32 lanes apart, which coalesce, and hands each
+// lane its 16 neighbouring columns through shared memory (`stage`, 512 elements
+// of the warp).  left: bytes of the row from the strip's start on.
+template <int DT> constexpr int strip_bytes() { return 512 * dtype_size(DT); }
+
+template <int DT, int PB>
+__device__ __forceinline__ void load_strip(const uint8_t *strip, int64_t left, int lane, Raw16<DT> &r)
+{
+    constexpr int WORDS = 4 * dtype_size(DT);
+    uint32_t w[WORDS];
+    auto half = [&](int64_t o) {
+        return o + 2 <= left ? static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(strip + o))) : 0u;
+    };
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+        if constexpr (PB == 4) {
+            const int64_t o = (i * 32 + lane) * 4;
+            w[i] = o + 4 <= left ? __ldg(reinterpret_cast<const uint32_t *>(strip + o)) : dtype_size(DT) == 2 ? half(o) : 0u;
+        } else {
+            w[i] = half((2 * i * 32 + lane) * 2) | (half(((2 * i + 1) * 32 + lane) * 2) << 16);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < dtype_size(DT); ++i) r.v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+template <int DT, int PB>
+__device__ __forceinline__ void pieces_to_columns(uint8_t *stage, int lane, Raw16<DT> &r)
+{
+    constexpr int SZ = dtype_size(DT);
+#pragma unroll
+    for (int i = 0; i < SZ; ++i) {
+        const uint32_t w[4] = {r.v[i].x, r.v[i].y, r.v[i].z, r.v[i].w};
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int k = 4 * i + t;
+            if constexpr (PB == 4) {
+                reinterpret_cast<uint32_t *>(stage)[k * 32 + lane] = w[t];
+            } else {
+                reinterpret_cast<uint16_t *>(stage)[2 * k * 32 + lane] = static_cast<uint16_t>(w[t]);
+                reinterpret_cast<uint16_t *>(stage)[(2 * k + 1) * 32 + lane] = static_cast<uint16_t>(w[t] >> 16);
+            }
+        }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < SZ; ++i) r.v[i] = reinterpret_cast<const uint4 *>(stage + lane * 16 * SZ)[i];
+    __syncwarp();
+}
+
+// The reverse: each lane's 16 rounded values leave in coalesced pieces.
+template <int DT, int PB>
+__device__ __forceinline__ void store_strip(uint8_t *stage, uint8_t *strip, int64_t left, int lane, const float (&f)[16])
+{
+    constexpr int WORDS = 4 * dtype_size(DT);
+    store16<DT, 16>(stage, lane * 16, 512, f);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < (PB == 4 ? WORDS : 2 * WORDS); ++i) {
+        const int o = (i * 32 + lane) * PB;
+        if (PB == 4 && o + 4 <= left) *reinterpret_cast<uint32_t *>(strip + o) = *reinterpret_cast<const uint32_t *>(stage + o);
+        else if (dtype_size(DT) == 2 && o + 2 <= left)
+            *reinterpret_cast<uint16_t *>(strip + o) = *reinterpret_cast<const uint16_t *>(stage + o);
+    }
+    __syncwarp();
+}
+
 // ---------------------------------------------------------------------------
 // Rows and columns of a block of 32 x 8 threads: a warp covers 512 columns (16
 // a lane: an NVFP4 block, half an MXFP4 block), a thread the four rows r, r +
@@ -335,9 +403,17 @@ template <int DT, int VEC>
 __device__ __forceinline__ void load_rows(const QuantArgs &a, int64_t r, int64_t c, Raw16<DT> (&raw)[QROWS])
 {
 #pragma unroll
-    for (int u = 0; u < QROWS; ++u)
-        if (r + 32 * u < a.rows)
-            load16<DT, VEC>(static_cast<const uint8_t *>(a.x) + (r + 32 * u) * a.ld * dtype_size(DT), c, a.K, raw[u]);
+    for (int u = 0; u < QROWS; ++u) {
+        if (r + 32 * u >= a.rows) break;
+        const uint8_t *row = static_cast<const uint8_t *>(a.x) + (r + 32 * u) * a.ld * dtype_size(DT);
+        if constexpr (VEC >= 16) {
+            load16<DT, VEC>(row, c, a.K, raw[u]);
+        } else {
+            const int lane = threadIdx.x;
+            const int64_t c0 = c - lane * 16;               // the strip's first column
+            load_strip<DT, VEC>(row + c0 * dtype_size(DT), (a.K - c0) * dtype_size(DT), lane, raw[u]);
+        }
+    }
 }
 
 template <int DT, int VEC, int FMT>
@@ -346,6 +422,7 @@ __global__ void __launch_bounds__(QTX *QTY) k_fp4_quant(const QuantArgs a)
     constexpr int TILE_K = FmtT<FMT>::TILE_K;
     constexpr int LB = FMT == FMT_MX ? 2 : 1;               // lanes per block
     __shared__ float4 s_cs[4][QTX];                         // the strip's factors, [4 columns][lane]
+    __shared__ __align__(16) uint8_t s_stage[VEC < 16 ? QTY * strip_bytes<DT>() : 16];
     const int lane = threadIdx.x;
     const int64_t c = (static_cast<int64_t>(blockIdx.x) * QTX + lane) * 16;
     const int64_t ktiles = scale_tiles_k(FMT, a.K), qld = code_row_bytes(a.K);
@@ -387,6 +464,7 @@ __global__ void __launch_bounds__(QTX *QTY) k_fp4_quant(const QuantArgs a)
                 const int64_t row = r + 32 * u;
                 if (row >= a.rows) break;
                 float f[16];
+                if constexpr (VEC < 16) pieces_to_columns<DT, VEC>(s_stage + threadIdx.y * strip_bytes<DT>(), lane, raw[u]);
                 widen16<DT>(raw[u], f);
                 float m = 0.0f;
 #pragma unroll
@@ -445,14 +523,16 @@ __global__ void __launch_bounds__(QTX *QTY) k_fp4_dequant(const DequantArgs a)
     const int64_t ktiles = scale_tiles_k(FMT, a.K), qld = code_row_bytes(a.K);
     pdl_wait();
     const float g = (FMT == FMT_NV && a.g != nullptr) ? __ldg(a.g) : 1.0f;
-    if (c < a.K) {
+    __shared__ __align__(16) uint8_t s_stage[VEC < 16 ? QTY * strip_bytes<DT>() : 16];
+    const bool in = c < a.K;
+    if (VEC < 16 || in) {                                   // narrow stores take the whole warp
         const int64_t kt = c / TILE_K;
         const int shift = 8 * (static_cast<int>(c % TILE_K) / FmtT<FMT>::BLOCK);
         uint4 w = make_uint4(0u, 0u, 0u, 0u);               // the four rows' scale words (inside the tile, used or not)
-        uint2 next[QROWS];
+        uint2 next[QROWS] = {};
         auto load = [&](int64_t unit) {
             const int64_t r = unit_row(unit, threadIdx.y);
-            if (unit >= a.units || r >= a.rows) return;
+            if (unit >= a.units || r >= a.rows || !in) return;
             w = __ldg(reinterpret_cast<const uint4 *>(a.sf + scale_word(r, kt, ktiles)));
 #pragma unroll
             for (int u = 0; u < QROWS; ++u)
@@ -482,7 +562,13 @@ __global__ void __launch_bounds__(QTX *QTY) k_fp4_dequant(const DequantArgs a)
                     f[i] = t.x;
                     f[i + 1] = t.y;
                 }
-                store16<DT, VEC>(static_cast<uint8_t *>(a.out) + row * a.K * SZ, c, a.K, f);
+                uint8_t *out = static_cast<uint8_t *>(a.out) + row * a.K * SZ;
+                if constexpr (VEC >= 16) {
+                    store16<DT, VEC>(out, c, a.K, f);
+                } else {
+                    const int64_t c0 = c - threadIdx.x * 16;
+                    store_strip<DT, VEC>(s_stage + threadIdx.y * strip_bytes<DT>(), out + c0 * SZ, (a.K - c0) * SZ, threadIdx.x, f);
+                }
             }
         }
     }

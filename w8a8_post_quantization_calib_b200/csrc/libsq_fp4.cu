@@ -72,7 +72,8 @@ cudaError_t launch_quant_vec(const fp4::QuantArgs &a, int fmt, cudaStream_t st)
     if (vec == 32) return launch_quant_fmt<DT, 32>(a, fmt, st);
     if (vec == 16) return launch_quant_fmt<DT, 16>(a, fmt, st);
     if (vec >= 4) return launch_quant_fmt<DT, 4>(a, fmt, st);
-    return launch_quant_fmt<DT, 0>(a, fmt, st);
+    if constexpr (DT != DT_F32) return launch_quant_fmt<DT, 2>(a, fmt, st);
+    return cudaErrorInvalidValue;      // fp32 rows are 4-byte aligned
 }
 
 sq_status quant_fp4(const void *x, int dt, int64_t rows, int64_t K, int64_t ld, const float *s, int weight, int fmt,
@@ -108,7 +109,8 @@ cudaError_t launch_dequant_vec(const fp4::DequantArgs &a, int fmt, cudaStream_t 
     if (vec == 32) return launch_dequant<DT, 32>(a, fmt, st);
     if (vec == 16) return launch_dequant<DT, 16>(a, fmt, st);
     if (vec >= 4) return launch_dequant<DT, 4>(a, fmt, st);
-    return launch_dequant<DT, 0>(a, fmt, st);
+    if constexpr (DT != DT_F32) return launch_dequant<DT, 2>(a, fmt, st);
+    return cudaErrorInvalidValue;      // fp32 rows are 4-byte aligned
 }
 
 // ------------------------------------------------------------------ product
