@@ -48,46 +48,49 @@ struct WriteArgs {
     const int64_t *slots;      // [T]; a negative slot is skipped
     uint8_t *kc, *vc;
     void *ks, *vs;
-    int H, D, groups;          // groups: warps a token (heads / heads per warp)
-    int lph_log2, vec;         // lanes a row; bytes a load (32, 16, 0: single elements)
+    int H, D;
+    int lph_log2, vec;         // lanes a row; bytes a load (32, 16, 8, 4, 0: single elements)
+    uint64_t head_inv;         // ceil(2^63 / H): division by a product
 };
 
-// NCH: chunks of 16 elements a lane (2 only for D > 512); TOK: tokens a warp,
-// all their loads in flight before the first is computed.
+// Rows (token, head) laid end to end, 32 / lanes of them a step; keys and values
+// in turn by warps.  NCH: chunks of 16 elements a lane (2 only for D > 512); TOK:
+// steps a warp, all their loads in flight before the first is computed.
 constexpr int TOKENS = 2;
 
 template <int DT, int FMT, int VEC, int NCH, int TOK>
 __global__ void __launch_bounds__(WARPS * 32) k_kv_write(const WriteArgs a)
 {
     constexpr int SZ = dtype_size(DT);
-    const int lane = threadIdx.x & 31, lph = 1 << a.lph_log2, sub = lane & (lph - 1);
+    const int lane = threadIdx.x & 31, lph = 1 << a.lph_log2, sub = lane & (lph - 1), per = 32 >> a.lph_log2;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
-    const int64_t tb = unit / (2 * a.groups);
-    const int rest = static_cast<int>(unit - tb * (2 * a.groups));
-    const bool is_v = rest >= a.groups;
-    const int h = (is_v ? rest - a.groups : rest) * (32 >> a.lph_log2) + (lane >> a.lph_log2);
+    const bool is_v = unit & 1;
+    const int64_t rows = a.T * a.H;
     const int rb = row_bytes(FMT, a.D), sb = scale_bytes(FMT, a.D);
     pdl_wait();
     // the loads do not wait for the slots: a skipped token's row is read all the same
     fp4::Raw16<DT> raw[TOK][NCH];
     int64_t slot[TOK];
+    int h[TOK];
 #pragma unroll
     for (int k = 0; k < TOK; ++k) {
-        const int64_t t = tb * TOK + k;
-        const bool in = t < a.T && h < a.H;
-        slot[k] = t < a.T ? __ldg(a.slots + t) : -1;
+        const int64_t r = ((unit >> 1) * TOK + k) * per + (lane >> a.lph_log2);
+        // r < 2^47 and H <= 2^16: the error of the quotient, r / 2^63, is below 1 / H
+        const int64_t t = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(r) << 1, a.head_inv));
+        h[k] = static_cast<int>(r - t * a.H);
+        slot[k] = r < rows ? __ldg(a.slots + t) : -1;
         const void *src = static_cast<const uint8_t *>(is_v ? a.v : a.k) +
-                          (t * (is_v ? a.v_ld : a.k_ld) + static_cast<int64_t>(h) * a.D) * SZ;
+                          (t * (is_v ? a.v_ld : a.k_ld) + static_cast<int64_t>(h[k]) * a.D) * SZ;
 #pragma unroll
-        for (int i = 0; i < NCH; ++i) fp4::load16_rt<DT, VEC>(a.vec, src, (i * lph + sub) * 16, in ? a.D : 0, raw[k][i]);
+        for (int i = 0; i < NCH; ++i) fp4::load16_rt<DT, VEC>(a.vec, src, (i * lph + sub) * 16, r < rows ? a.D : 0, raw[k][i]);
     }
     uint8_t *const cache = is_v ? a.vc : a.kc;
     void *const scale = is_v ? a.vs : a.ks;
 #pragma unroll
     for (int k = 0; k < TOK; ++k) {
-        if (slot[k] >= a.num_slots && lane == 0) bad_index();
-        const bool live = slot[k] >= 0 && slot[k] < a.num_slots && h < a.H;
-        const int64_t row = slot[k] * a.H + h;
+        if (slot[k] >= a.num_slots && sub == 0) bad_index();
+        const bool live = slot[k] >= 0 && slot[k] < a.num_slots;
+        const int64_t row = slot[k] * a.H + h[k];
         float f[NCH][16];
         float m = 0.0f;
 #pragma unroll

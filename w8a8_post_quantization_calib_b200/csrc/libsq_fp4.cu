@@ -343,6 +343,9 @@ template <typename F> cudaError_t kv_dispatch(int dt, int fmt, int vec, F &&laun
 
 constexpr int KV_READ_WARPS = 16;
 
+// ceil(2^63 / d): the high word of (2 n) * inverse63(d) is n / d as long as n * d < 2^63
+inline uint64_t inverse63(int64_t d) { return ((uint64_t(1) << 63) + static_cast<uint64_t>(d) - 1) / static_cast<uint64_t>(d); }
+
 sq_status check_kv(int fmt, int dt, int64_t H, int64_t D)
 {
     if (!valid_kv(fmt) || !valid_dt(dt) || H <= 0 || D <= 0) return SQ_ERR_INVALID_ARG;
@@ -463,18 +466,19 @@ sq_status sq_kv_cache_write(const void *k, const void *v, sq_dtype dt, int64_t T
     if (T == 0) return SQ_OK;
     const int ll = lanes_log2(static_cast<int>(D));
     kv::WriteArgs a{k, v, T, k_ld, v_ld, num_slots, slots, static_cast<uint8_t *>(k_cache),
-                    static_cast<uint8_t *>(v_cache), k_scale, v_scale, static_cast<int>(H), static_cast<int>(D),
-                    static_cast<int>(cdiv(H, 32 >> ll)), ll, 0};
-    if (T > (int64_t(1) << 31) || cdiv(T * 2 * a.groups, kv::WARPS) >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
+                    static_cast<uint8_t *>(v_cache), k_scale, v_scale, static_cast<int>(H), static_cast<int>(D), ll, 0,
+                    inverse63(H)};
+    const int64_t steps = cdiv(T * H, 32 >> ll);                // of a warp, for keys and again for values
+    if (T > (int64_t(1) << 31) || cdiv(2 * steps, kv::WARPS) >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
     const int es = dtype_size(dt);
     a.vec = std::min(vec_bytes(k, (k_ld * es) | (D * es)), vec_bytes(v, (v_ld * es) | (D * es)));
     const cudaStream_t st = as_stream(stream);
-    // several tokens a warp once that leaves every SM its 64 warps
-    const bool many = T * 2 * a.groups >= static_cast<int64_t>(kv::TOKENS) * 64 * sm_count();
+    // several steps a warp once that leaves every SM its 64 warps
+    const bool many = 2 * steps >= static_cast<int64_t>(kv::TOKENS) * 64 * sm_count();
     const cudaError_t e = kv_dispatch(dt, fmt, a.vec, [&](auto d, auto f, auto w) {
         constexpr int DT = decltype(d)::value, FMT = decltype(f)::value, VEC = decltype(w)::value;
         const int64_t tok = D <= 512 && many ? kv::TOKENS : 1;
-        const dim3 grid(static_cast<unsigned>(cdiv(cdiv(T, tok) * 2 * a.groups, kv::WARPS))), block(kv::WARPS * 32);
+        const dim3 grid(static_cast<unsigned>(cdiv(2 * cdiv(steps, tok), kv::WARPS))), block(kv::WARPS * 32);
         if (D > 512) return launch_pdl(kv::k_kv_write<DT, FMT, VEC, 2, 1>, grid, block, 0, st, a);
         if (many) return launch_pdl(kv::k_kv_write<DT, FMT, VEC, 1, kv::TOKENS>, grid, block, 0, st, a);
         return launch_pdl(kv::k_kv_write<DT, FMT, VEC, 1, 1>, grid, block, 0, st, a);
@@ -512,9 +516,8 @@ sq_status sq_kv_cache_read(sq_kv_format fmt, const void *k_cache, const void *k_
     const int es = dtype_size(out_dt);
     a.vec = std::min(vec_bytes(k_out, D * es), vec_bytes(v_out, D * es));
     const cudaStream_t st = as_stream(stream);
-    auto inverse = [](int64_t d) { return ((uint64_t(1) << 63) + static_cast<uint64_t>(d) - 1) / static_cast<uint64_t>(d); };
-    a.page_inv = inverse(page_size);
-    a.head_inv = inverse(H);
+    a.page_inv = inverse63(page_size);
+    a.head_inv = inverse63(H);
     // Rows end to end where a warp a token would leave lanes idle or have one
     // group of heads in flight: 1 head of 64 414 -> 60 us (45 at the copy rate), 2
     // of 128 107 -> 58, 5 of 128 59 -> 48; 8 of 128 stay a warp a token (69 us
