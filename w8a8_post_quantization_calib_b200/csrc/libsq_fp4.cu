@@ -79,12 +79,12 @@ cudaError_t launch_quant_vec(const fp4::QuantArgs &a, int fmt, cudaStream_t st)
 sq_status quant_fp4(const void *x, int dt, int64_t rows, int64_t K, int64_t ld, const float *s, int weight, int fmt,
                     const float *g, uint8_t *q, uint8_t *sf, sq_stream stream)
 {
-    if (x == nullptr || q == nullptr || sf == nullptr || !valid_dt(dt) || !valid_fmt(fmt)) return SQ_ERR_INVALID_ARG;
-    if (rows < 0 || K <= 0 || ld < K) return SQ_ERR_INVALID_ARG;
+    if (!valid_dt(dt) || !valid_fmt(fmt) || rows < 0 || K <= 0 || ld < K) return SQ_ERR_INVALID_ARG;
+    if (rows == 0) return SQ_OK;               // empty tensors have no address
+    if (x == nullptr || q == nullptr || sf == nullptr) return SQ_ERR_INVALID_ARG;
     if (rows > (int64_t(1) << 40) || K > (int64_t(1) << 30) || ld > (int64_t(1) << 40)) return SQ_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(sf)) return SQ_ERR_MISALIGNED;
     if ((reinterpret_cast<uintptr_t>(x) & (dtype_size(dt) - 1)) != 0) return SQ_ERR_MISALIGNED;
-    if (rows == 0) return SQ_OK;
     fp4::QuantArgs a{x, rows, K, ld, s, g, q, sf, 0, weight};
     const cudaStream_t st = as_stream(stream);
     const cudaError_t e = dt == SQ_F32   ? launch_quant_vec<DT_F32>(a, fmt, st)
@@ -390,13 +390,12 @@ sq_status sq_smooth_quant_act_fp4(const void *x, sq_dtype dt, int64_t M, int64_t
 sq_status sq_dequant_fp4(const uint8_t *q4, const uint8_t *sf, sq_fp4_format fmt, int64_t rows, int64_t K,
                          const float *g, sq_dtype out_dt, void *out, sq_stream stream)
 {
-    if (q4 == nullptr || sf == nullptr || out == nullptr || !valid_fmt(fmt) || !valid_dt(out_dt))
-        return SQ_ERR_INVALID_ARG;
-    if (rows < 0 || K <= 0) return SQ_ERR_INVALID_ARG;
+    if (!valid_fmt(fmt) || !valid_dt(out_dt) || rows < 0 || K <= 0) return SQ_ERR_INVALID_ARG;
+    if (rows == 0) return SQ_OK;
+    if (q4 == nullptr || sf == nullptr || out == nullptr) return SQ_ERR_INVALID_ARG;
     if (rows > (int64_t(1) << 40) || K > (int64_t(1) << 30)) return SQ_ERR_UNSUPPORTED;
     if (!aligned16(q4) || !aligned16(sf)) return SQ_ERR_MISALIGNED;
     if ((reinterpret_cast<uintptr_t>(out) & (dtype_size(out_dt) - 1)) != 0) return SQ_ERR_MISALIGNED;
-    if (rows == 0) return SQ_OK;
     fp4::DequantArgs a{q4, sf, rows, K, g, out, 0};
     const cudaStream_t st = as_stream(stream);
     const cudaError_t e = out_dt == SQ_F32   ? launch_dequant_vec<DT_F32>(a, fmt, st)
@@ -409,16 +408,14 @@ sq_status sq_linear_fp4(const uint8_t *xq4, const uint8_t *x_sf, const uint8_t *
                         sq_fp4_format fmt, int64_t M, int64_t N, int64_t K, const float *g_act, const float *g_w,
                         const void *bias, sq_dtype out_dt, void *y, sq_stream stream)
 {
-    if (xq4 == nullptr || x_sf == nullptr || wq4 == nullptr || w_sf == nullptr || y == nullptr || !valid_fmt(fmt) ||
-        !valid_dt(out_dt))
-        return SQ_ERR_INVALID_ARG;
-    if (M < 0 || N <= 0 || K <= 0) return SQ_ERR_INVALID_ARG;
+    if (!valid_fmt(fmt) || !valid_dt(out_dt) || M < 0 || N <= 0 || K <= 0) return SQ_ERR_INVALID_ARG;
+    if (M == 0) return SQ_OK;
+    if (xq4 == nullptr || x_sf == nullptr || wq4 == nullptr || w_sf == nullptr || y == nullptr) return SQ_ERR_INVALID_ARG;
     if (M > (int64_t(1) << 30) || N > (int64_t(1) << 30) || K > (int64_t(1) << 30)) return SQ_ERR_UNSUPPORTED;
     if (!aligned16(xq4) || !aligned16(x_sf) || !aligned16(wq4) || !aligned16(w_sf)) return SQ_ERR_MISALIGNED;
     if ((reinterpret_cast<uintptr_t>(y) & (dtype_size(out_dt) - 1)) != 0 ||
         (reinterpret_cast<uintptr_t>(bias) & (dtype_size(out_dt) - 1)) != 0)
         return SQ_ERR_MISALIGNED;
-    if (M == 0) return SQ_OK;
     fp4::Fp4Params fp{};
     gemm::Params &p = fp.p;
     p.M = static_cast<int>(M);
@@ -452,10 +449,11 @@ sq_status sq_kv_cache_write(const void *k, const void *v, sq_dtype dt, int64_t T
 {
     const sq_status r = check_kv(fmt, dt, H, D);
     if (r != SQ_OK) return r;
+    if (T < 0 || k_ld < H * D || v_ld < H * D || num_slots < 0) return SQ_ERR_INVALID_ARG;
+    if (T == 0) return SQ_OK;
     if (k == nullptr || v == nullptr || slots == nullptr || k_cache == nullptr || k_scale == nullptr ||
         v_cache == nullptr || v_scale == nullptr)
         return SQ_ERR_INVALID_ARG;
-    if (T < 0 || k_ld < H * D || v_ld < H * D || num_slots < 0) return SQ_ERR_INVALID_ARG;
     if (num_slots > (int64_t(1) << 40) || k_ld > (int64_t(1) << 32) || v_ld > (int64_t(1) << 32))
         return SQ_ERR_UNSUPPORTED;
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale))
@@ -463,7 +461,6 @@ sq_status sq_kv_cache_write(const void *k, const void *v, sq_dtype dt, int64_t T
     if (((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & (dtype_size(dt) - 1)) != 0 ||
         (reinterpret_cast<uintptr_t>(slots) & 7) != 0)
         return SQ_ERR_MISALIGNED;
-    if (T == 0) return SQ_OK;
     const int ll = lanes_log2(static_cast<int>(D));
     kv::WriteArgs a{k, v, T, k_ld, v_ld, num_slots, slots, static_cast<uint8_t *>(k_cache),
                     static_cast<uint8_t *>(v_cache), k_scale, v_scale, static_cast<int>(H), static_cast<int>(D), ll, 0,
@@ -494,10 +491,11 @@ sq_status sq_kv_cache_read(sq_kv_format fmt, const void *k_cache, const void *k_
 {
     const sq_status r = check_kv(fmt, out_dt, H, D);
     if (r != SQ_OK) return r;
+    if (num_pages < 0 || page_size <= 0 || B < 0 || max_pages < 0 || total < 0) return SQ_ERR_INVALID_ARG;
+    if (total == 0 || B == 0) return SQ_OK;
     if (k_cache == nullptr || k_scale == nullptr || v_cache == nullptr || v_scale == nullptr || table == nullptr ||
         cu_rows == nullptr || k_out == nullptr || v_out == nullptr)
         return SQ_ERR_INVALID_ARG;
-    if (num_pages < 0 || page_size <= 0 || B < 0 || max_pages < 0 || total < 0) return SQ_ERR_INVALID_ARG;
     if (num_pages >= (int64_t(1) << 31) || page_size >= (int64_t(1) << 31) || B >= (int64_t(1) << 30) ||
         max_pages >= (int64_t(1) << 31) || total >= (int64_t(1) << 31))
         return SQ_ERR_UNSUPPORTED;
@@ -507,7 +505,6 @@ sq_status sq_kv_cache_read(sq_kv_format fmt, const void *k_cache, const void *k_
         ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(cu_rows) |
           reinterpret_cast<uintptr_t>(starts)) & 3) != 0)
         return SQ_ERR_MISALIGNED;
-    if (total == 0 || B == 0) return SQ_OK;
     const int ll = lanes_log2(static_cast<int>(D));
     kv::ReadArgs a{static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), k_scale, v_scale,
                    num_pages, max_pages, table, cu_rows, starts, total, k_out, v_out, static_cast<int>(B),

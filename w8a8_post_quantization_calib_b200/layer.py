@@ -1,4 +1,5 @@
-"""Layer-level driver of the SmoothQuant W8A8 linear on top of the C ABI.
+"""Layer-level drivers on top of the C ABI: the SmoothQuant W8A8 linear, the same
+layer in 4-bit microscaled formats, and the paged key/value cache in 8 or 4 bits.
 
 Mirrors the calibration -> offline transform -> runtime flow of the
 "010. SmoothQuant Integration" design (SmoothQuantQuantizer.add_batch keeps
@@ -12,8 +13,10 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (ACT_PER_TOKEN, ACT_STATIC, calib_absmax, linear_w8a8, linear_workspace_size, quant_weight,
-               smooth_quant_act, smooth_scales)
+from . import (ACT_PER_TOKEN, ACT_STATIC, KV_INT8, KV_MXFP4, MXFP4, NVFP4, calib_absmax, fp4_code_bytes,
+               fp4_scale_bytes, kv_cache_read, kv_cache_write, kv_row_bytes, kv_scale_bytes, linear_fp4, linear_w8a8,
+               linear_workspace_size, quant_weight, quant_weight_fp4, smooth_quant_act, smooth_quant_act_fp4,
+               smooth_scales, smooth_scales_nvfp4)
 
 
 class Calibrator:
@@ -86,4 +89,83 @@ class QuantizedLinear:
         return y
 
 
-__all__ = ["Calibrator", "QuantizedLinear", "ACT_STATIC", "ACT_PER_TOKEN"]
+@dataclass
+class QuantizedLinearFp4:
+    """The smoothed layer with 4-bit weights and activations (format MXFP4 or NVFP4)."""
+    wq4: torch.Tensor         # uint8 [N, fp4_code_bytes(K)]
+    w_sf: torch.Tensor        # uint8, tiled block scales
+    s: torch.Tensor           # fp32 [K]
+    fmt: int
+    K: int
+    g_act: torch.Tensor | None = None      # NVFP4: tensor scales, fp32 [1]
+    g_w: torch.Tensor | None = None
+    bias: torch.Tensor | None = None
+
+    @property
+    def N(self) -> int:
+        return self.wq4.shape[0]
+
+    @classmethod
+    def from_float(cls, w: torch.Tensor, act_max: torch.Tensor, alpha: float = 0.5, fmt: int = MXFP4, bias=None,
+                   stream=None) -> "QuantizedLinearFp4":
+        N, K = w.shape
+        dev = w.device
+        w_max = torch.zeros(K, dtype=torch.float32, device=dev)
+        calib_absmax(w, w_max, stream=stream)
+        s = torch.empty(K, dtype=torch.float32, device=dev)
+        g_act = g_w = None
+        if fmt == NVFP4:
+            g_act, g_w = (torch.empty(1, dtype=torch.float32, device=dev) for _ in range(2))
+        smooth_scales_nvfp4(act_max, w_max, alpha, s, g_act, g_w, stream=stream)
+        wq4 = torch.empty(N, fp4_code_bytes(K), dtype=torch.uint8, device=dev)
+        w_sf = torch.empty(fp4_scale_bytes(fmt, N, K), dtype=torch.uint8, device=dev)
+        quant_weight_fp4(w, s, fmt, wq4, w_sf, g=g_w, stream=stream)
+        return cls(wq4, w_sf, s, fmt, K, g_act, g_w, bias)
+
+    def quantize_input(self, x: torch.Tensor, xq4=None, x_sf=None, stream=None):
+        M = x.shape[0]
+        if xq4 is None:
+            xq4 = torch.empty(M, fp4_code_bytes(self.K), dtype=torch.uint8, device=x.device)
+        if x_sf is None:
+            x_sf = torch.empty(fp4_scale_bytes(self.fmt, max(M, 1), self.K), dtype=torch.uint8, device=x.device)
+        smooth_quant_act_fp4(x, self.s, self.fmt, xq4, x_sf, g=self.g_act, stream=stream)
+        return xq4, x_sf
+
+    def forward(self, x: torch.Tensor, out_dtype=torch.bfloat16, y=None, stream=None):
+        xq4, x_sf = self.quantize_input(x, stream=stream)
+        if y is None:
+            y = torch.empty(x.shape[0], self.N, dtype=out_dtype, device=x.device)
+        linear_fp4(xq4, x_sf, self.wq4, self.w_sf, self.fmt, y, bias=self.bias, g_act=self.g_act, g_w=self.g_w,
+                   stream=stream)
+        return y
+
+
+class PagedKVCache:
+    """Keys and values of H heads of D elements in num_pages pages of page_size tokens (slot = page * page_size +
+    position in the page), quantised as they are written."""
+
+    def __init__(self, num_pages: int, page_size: int, H: int, D: int, fmt: int = KV_INT8, device="cuda"):
+        self.num_pages, self.page_size, self.H, self.D, self.fmt = num_pages, page_size, H, D, fmt
+        codes = torch.int8 if fmt == KV_INT8 else torch.uint8
+        shape = (num_pages, page_size, H)
+        self.k, self.v = (torch.zeros(*shape, kv_row_bytes(fmt, D), dtype=codes, device=device) for _ in range(2))
+        if fmt == KV_MXFP4:
+            self.k_scale, self.v_scale = (torch.zeros(*shape, kv_scale_bytes(fmt, D), dtype=torch.uint8, device=device)
+                                          for _ in range(2))
+        else:
+            self.k_scale, self.v_scale = (torch.zeros(shape, dtype=torch.float32, device=device) for _ in range(2))
+
+    def write(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+        """k, v: [T, H, D]; slots: int64 [T], a negative one is skipped."""
+        kv_cache_write(k, v, slots, self.fmt, self.k, self.k_scale, self.v, self.v_scale, stream=stream)
+
+    def read(self, table: torch.Tensor, cu_rows: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor, starts=None,
+             stream=None):
+        """Rows cu_rows[b] .. cu_rows[b + 1] - 1 of the outputs [total, H, D] take sequence b's positions from starts[b]
+        (0 without) on."""
+        kv_cache_read(self.fmt, self.k, self.k_scale, self.v, self.v_scale, table, cu_rows, k_out, v_out, starts=starts,
+                      stream=stream)
+        return k_out, v_out
+
+
+__all__ = ["Calibrator", "QuantizedLinear", "QuantizedLinearFp4", "PagedKVCache", "ACT_STATIC", "ACT_PER_TOKEN"]
