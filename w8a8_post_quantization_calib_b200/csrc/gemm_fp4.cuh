@@ -174,7 +174,7 @@ __device__ __forceinline__ float out_factor(const Fp4Params &fp)
 
 // ---------------------------------------------------------------------------
 // Few tiles: A = weights [N, K], B = activations [M, K] in tiles of BN tokens
-// (more than one for BN = 128 only); a TMEM lane is an output channel, a column
+// (more than one for BN = 64 and 128 only); a TMEM lane is an output channel, a column
 // a token.  A cluster of CS
 // CTAs shares a weight tile's K range; two CTAs fit an SM.  The partial sums
 // are reduced by the whole cluster: groups of four tokens are dealt out to the
@@ -231,6 +231,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 2)
 {
     using C = SwapCfg<BN, FMT>;
     using Sf = SfT<FMT>;
+    // A scale address has to lie on an even TMEM column (64 rows): narrower
+    // tiles than 64 tokens come alone (M <= BN).
     static_assert((CS - 1) * ((BN / 4 + CS - 1) / CS) * 2048 <= C::stages(2) * C::STAGE_BYTES, "partial sums must fit the stages");
     const Params &p = fp.p;
     const int S = p.ring;                                  // stages
@@ -313,7 +315,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 2)
                 ptx::tma_load_2d(sa, &map_w, fb, kb * BKB, tile * BM);
                 ptx::tma_load_3d(ssa, &map_ws, fb, 0, kb * Sf::TILES, tile);
                 ptx::tma_load_2d(sb, &map_x, fb, kb * BKB, tc * BN);
-                ptx::tma_load_3d(ssb, &map_xs, fb, 0, kb * Sf::TILES, tc);
+                ptx::tma_load_3d(ssb, &map_xs, fb, 0, kb * Sf::TILES, tc * BN / 128);
             }
             __syncwarp();
             ++issued;
@@ -333,7 +335,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 2)
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        const uint32_t sfa0 = tmem_base + BN, sfb0 = sfa0 + C::SF_COLS;
+        // a tile's tokens start in the middle of a scale tile: 32 rows a TMEM column
+        const uint32_t sfa0 = tmem_base + BN, sfb0 = sfa0 + C::SF_COLS, shift = (tc * BN) % 128 / 32;
         for (int kb = kb_begin; kb < kb_end; ++kb) {
             ok = wait(full_bar(stage), phase, ERR_MMA + 1);
             if (!ok) break;
@@ -351,7 +354,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 2)
                 for (int k = 0; k < 4; ++k) {
                     const int t = k / Sf::MMAS;
                     mma_fp4<FMT, 1>(tmem_base, ad + 2 * k, bd + 2 * k, idesc_fp4<FMT>(128, BN, (k % Sf::MMAS) * 2),
-                                    sfa0 + 4 * t, sfb0 + 4 * t, (kb > kb_begin || k > 0) ? 1u : 0u);
+                                    sfa0 + 4 * t, sfb0 + 4 * t + shift, (kb > kb_begin || k > 0) ? 1u : 0u);
                 }
                 ptx::tc_commit(empty_bar(stage));
             }

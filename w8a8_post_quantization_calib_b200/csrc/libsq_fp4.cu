@@ -200,29 +200,77 @@ inline int swap_cluster(int64_t tiles, int64_t num_kb)
     return cs;
 }
 
-// Whether few tiles and a long K make the cluster split over K faster than CTA
-// pairs for M > 128: M = 256, N = 512, K = 4096 6.1 us (pairs 8.9), K = 2048 5.9
-// (6.9), K = 512 5.4 (5.4); M = 256, N = 4096, K = 4096 8.3 (9.5), K = 1024 6.4 (6.0).
-inline bool swap_for_long_k(int64_t M, int64_t N, int64_t num_kb)
+// How the weights-as-A kernel would run a product: tokens a tile, CTAs a
+// cluster, and an estimate in us (below 0: not at all).
+struct SwapPlan {
+    int bn, cs;
+    double us;
+};
+
+// Up to 64 tokens one tile; above, tiles of 64 or 128 tokens as long as all
+// CTAs run at once (with M <= 128 the weights of one tile of 128 may take more
+// waves).  The estimate, fitted to M = 64..2048, N = 64..11008, K = 256..11008 on
+// B200: a start, K blocks of 256 elements, and the epilogue, which grows with
+// the tile.  M = 128, N = 512, K = 512: 4.2 us with tiles of 64, 5.5 with 128;
+// M = 128, N = 4096, K = 11008: 10.6 and 9.2 (clusters of 2 and 4).
+inline SwapPlan plan_swap(int64_t M, int64_t N, int64_t num_kb)
 {
-    const int cs = swap_cluster(cdiv(N, gemm::BM) * cdiv(M, 128), num_kb);
-    return (cs >= 4 && num_kb >= 8) || (cs == 2 && num_kb >= 16);
+    const int64_t tr = cdiv(N, gemm::BM);
+    if (M <= 64) {
+        const int bn = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+        return {bn, swap_cluster(tr, num_kb), 0.0};
+    }
+    SwapPlan best{128, 1, -1.0};
+    for (const int bn : {64, 128}) {
+        const int64_t tiles = tr * cdiv(M, bn);
+        const int cs = swap_cluster(tiles, num_kb);
+        if (tiles * cs > sm_count() && !(bn == 128 && M <= 128)) continue;
+        const double us = 2.4 + (cs > 1 ? 0.9 : 0.0) + static_cast<double>(num_kb) / cs * (bn == 64 ? 0.275 : 0.31) +
+                          (bn == 64 ? 1.3 : 2.6);
+        if (best.us < 0 || us < best.us) best = {bn, cs, us};
+    }
+    return best;
 }
 
 template <int FMT>
-sq_status dispatch_fp4_swap(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_t st)
+sq_status run_fp4_swap(fp4::Fp4Params fp, const Fp4Operands &o, const SwapPlan &plan, cudaStream_t st)
 {
     gemm::Params &p = fp.p;
     p.tiles_r = static_cast<int>(cdiv(p.N, gemm::BM));
-    p.tiles_c = static_cast<int>(cdiv(p.M, 128));
+    p.tiles_c = static_cast<int>(cdiv(p.M, plan.bn));
     p.num_kb = static_cast<int>(cdiv(o.row_bytes, 128));
     p.timeout_ns = g_timeout_ns;
     p.inject = g_inject & 1;
-    const int cs = swap_cluster(static_cast<int64_t>(p.tiles_r) * p.tiles_c, p.num_kb);
-    if (p.M <= 16) return launch_fp4_swap_cs<16, FMT>(fp, o, cs, st);
-    if (p.M <= 32) return launch_fp4_swap_cs<32, FMT>(fp, o, cs, st);
-    if (p.M <= 64) return launch_fp4_swap_cs<64, FMT>(fp, o, cs, st);
-    return launch_fp4_swap_cs<128, FMT>(fp, o, cs, st);
+    if (plan.bn == 16) return launch_fp4_swap_cs<16, FMT>(fp, o, plan.cs, st);
+    if (plan.bn == 32) return launch_fp4_swap_cs<32, FMT>(fp, o, plan.cs, st);
+    if (plan.bn == 64) return launch_fp4_swap_cs<64, FMT>(fp, o, plan.cs, st);
+    return launch_fp4_swap_cs<128, FMT>(fp, o, plan.cs, st);
+}
+
+// How CTA pairs would run it: tile columns and an estimate in us, the start
+// included.  Measured on B200 over M = 129..4096, N = 1024..28672, K =
+// 1024..11008: waves x (K blocks x time a block + time a tile).  A K block costs
+// a narrow tile almost what it costs a wide one, so narrow tiles pay where they
+// save a wave: M = 512, N = 12288, K = 4096 takes 16.7 / 14.9 / 19.0 us with 256
+// / 192 / 128 columns, M = 1024, N = 4096, K = 4096 11.4 / 14.8 / 14.7, M = 256,
+// N = 4096, K = 1024 7.1 / 6.5 / 6.1.
+struct PairPlan {
+    int bn;
+    double us;
+};
+
+inline PairPlan plan_pair(int64_t M, int64_t N, int64_t num_kb)
+{
+    const int64_t clusters = std::max(1, sm_count() / 2);
+    const int widths[3] = {256, 192, 128};
+    const double per_kb[3] = {0.35, 0.285, 0.275}, per_tile[3] = {1.1, 0.75, 0.35};
+    PairPlan best{256, -1.0};
+    for (int i = 0; i < 3; ++i) {
+        const int64_t tiles = cdiv(M, 2 * gemm::BM) * cdiv(N, widths[i]);
+        const double us = 4.55 + static_cast<double>(cdiv(tiles, clusters)) * (static_cast<double>(num_kb) * per_kb[i] + per_tile[i]);
+        if (best.us < 0 || us < best.us) best = {widths[i], us};
+    }
+    return best;
 }
 
 template <int BN, int KBO, int FMT>
@@ -280,29 +328,14 @@ sq_status launch_fp4_pair(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_t 
 }
 
 template <int FMT>
-sq_status dispatch_fp4_pair(const fp4::Fp4Params &fp, const Fp4Operands &o, cudaStream_t st)
+sq_status dispatch_fp4(const fp4::Fp4Params &fp, const Fp4Operands &o, cudaStream_t st)
 {
-    // The tile width with the least estimated time: waves x (K blocks x time a
-    // block + time a tile), in us as measured on B200 over M = 129..4096, N =
-    // 1024..28672, K = 1024..11008.  A K block costs a narrow tile almost what
-    // it costs a wide one, so narrow tiles pay where they save a wave: M =
-    // 512, N = 12288, K = 4096 takes 16.7 / 14.9 / 19.0 us with 256 / 192 /
-    // 128 columns, M = 1024, N = 4096, K = 4096 11.4 / 14.8 / 14.7, M = 256,
-    // N = 4096, K = 1024 7.1 / 6.5 / 6.1.
-    const int64_t clusters = std::max(1, sm_count() / 2), kb = cdiv(o.row_bytes, 128);
-    const int cands[3] = {256, 192, 128};
-    const double per_kb[3] = {0.35, 0.285, 0.275}, per_tile[3] = {1.1, 0.75, 0.35};
-    int best = 256;
-    double best_cost = -1.0;
-    for (int i = 0; i < 3; ++i) {
-        const int64_t tiles = cdiv(fp.p.M, 2 * gemm::BM) * cdiv(fp.p.N, cands[i]);
-        const double cost = static_cast<double>(cdiv(tiles, clusters)) * (static_cast<double>(kb) * per_kb[i] + per_tile[i]);
-        if (best_cost < 0 || cost < best_cost) {
-            best = cands[i];
-            best_cost = cost;
-        }
-    }
-    switch (best) {
+    const int64_t M = fp.p.M, N = fp.p.N, kb = cdiv(o.row_bytes, 128);
+    const SwapPlan swap = plan_swap(M, N, kb);
+    if (M <= 128) return run_fp4_swap<FMT>(fp, o, swap, st);
+    const PairPlan pair = plan_pair(M, N, kb);
+    if (swap.us >= 0 && swap.us < pair.us) return run_fp4_swap<FMT>(fp, o, swap, st);
+    switch (pair.bn) {
     case 256: return launch_fp4_pair<256, 1, FMT>(fp, o, st);
     case 192: return launch_fp4_pair<192, 1, FMT>(fp, o, st);
     default: return launch_fp4_pair<128, 1, FMT>(fp, o, st);
@@ -428,9 +461,7 @@ sq_status sq_linear_fp4(const uint8_t *xq4, const uint8_t *x_sf, const uint8_t *
     fp.g_w = fmt == SQ_NVFP4 ? g_w : nullptr;
     const Fp4Operands o{xq4, x_sf, wq4, w_sf, fp4::code_row_bytes(K), fp4::scale_tiles_k(fmt, K)};
     const cudaStream_t st = as_stream(stream);
-    if (M <= 128 || swap_for_long_k(M, N, cdiv(o.row_bytes, 128)))
-        return fmt == SQ_MXFP4 ? dispatch_fp4_swap<fp4::FMT_MX>(fp, o, st) : dispatch_fp4_swap<fp4::FMT_NV>(fp, o, st);
-    return fmt == SQ_MXFP4 ? dispatch_fp4_pair<fp4::FMT_MX>(fp, o, st) : dispatch_fp4_pair<fp4::FMT_NV>(fp, o, st);
+    return fmt == SQ_MXFP4 ? dispatch_fp4<fp4::FMT_MX>(fp, o, st) : dispatch_fp4<fp4::FMT_NV>(fp, o, st);
 }
 
 size_t sq_kv_row_bytes(sq_kv_format fmt, int64_t D)
