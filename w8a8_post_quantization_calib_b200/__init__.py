@@ -1,7 +1,8 @@
 """SmoothQuant W8A8 linear layer for NVIDIA B200 (sm_100a).
 
 Thin Python binding of ``libsq.so`` (the CUDA kernels behind the C ABI of
-``include/sq.h``).  The functions here only marshal arguments: they take
+``include/sq.h``; the 4-bit and key/value calls through the native module
+``_sqbind``).  The functions here only marshal arguments: they take
 CUDA ``torch.Tensor`` objects (PyTorch supplies device memory and streams),
 pass raw pointers and sizes to the library, and raise ``SQError`` on a
 non-OK status.  Every step of the layer runs in the library's kernels; there
@@ -183,7 +184,8 @@ def set_wait_timeout_ns(ns: int) -> None:
 
 
 def sync_status(stream=None) -> int:
-    """Synchronise the stream; returns the status (0 = OK, 5 = a barrier wait timed out)."""
+    """Synchronise the stream; returns the status (0 = OK, 5 = a barrier wait timed out, 1 = a key/value call met an index
+    outside the cache)."""
     return int(_lib.sq_sync_status(_stream(stream)))
 
 
