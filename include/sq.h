@@ -101,9 +101,9 @@ void sq_debug_inject(int what);
 
 /* Synchronises `stream`, then returns SQ_ERR_TIMEOUT if any kernel of this
  * library recorded a barrier timeout on the current device since the last
- * check (and clears the record), SQ_ERR_INVALID_ARG if a kernel of the
- * key/value cache met an index outside the cache, SQ_ERR_CUDA if the stream reported an error,
- * else SQ_OK. */
+ * check, SQ_ERR_INVALID_ARG if a kernel of the key/value cache met an index
+ * outside the cache since then (both records are cleared), SQ_ERR_CUDA if the
+ * stream reported an error, else SQ_OK. */
 sq_status sq_sync_status(sq_stream stream);
 
 /* -------------------------------------------------------------------------

@@ -304,6 +304,46 @@ def test_layer_in_a_graph_on_another_stream(fmt, M):
     _sync()
 
 
+@pytest.mark.parametrize("M,N,K", [(33, 512, 8192), (100, 1024, 11008), (300, 512, 4096), (700, 4096, 1024)])
+def test_two_streams_at_once_and_repeats(M, N, K):
+    """Calls on two streams side by side, and again, give the bits of a call alone (sums in a fixed order)."""
+    r = np.random.default_rng(M)
+    ops = []
+    for rows in (M, N):
+        q = dev(r.integers(0, 256, (rows, K // 2)).astype(np.uint8))
+        ops += [q, dev(r.integers(20, 60, sq.fp4_scale_bytes(NV, rows, K)).astype(np.uint8))]
+    want = torch.empty(M, N, device="cuda")
+    sq.linear_fp4(*ops, NV, want)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.empty(M, N, device="cuda") for _ in range(6)] for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(6):
+        for st, o in zip(streams, outs):
+            sq.linear_fp4(*ops, NV, o[i], stream=st)
+    torch.cuda.synchronize()
+    _sync()
+    assert all(torch.equal(o, want) for ys in outs for o in ys)
+
+
+def test_timeout_is_not_hidden_by_a_bad_index():
+    """Both records of the device are kept: the timeout is reported first, then neither."""
+    assert sq.sync_status() == 0
+    c = torch.zeros(1, 1, 1, 16, dtype=torch.int8, device="cuda")
+    s = torch.zeros(1, 1, 1, device="cuda")
+    k = torch.zeros(1, 1, 16, device="cuda")
+    sq.kv_cache_write(k, k, torch.tensor([5], device="cuda"), sq.KV_INT8, c, s, c.clone(), s.clone())
+    sq.set_wait_timeout_ns(20_000_000)
+    sq.lib().sq_debug_inject(1)
+    try:
+        q, sf = _buffers(4, 512, MX, 0)
+        sq.linear_fp4(q, sf, q, sf, MX, torch.empty(4, 4, dtype=torch.bfloat16, device="cuda"))
+        assert sq.sync_status() == 5
+        assert sq.sync_status() == 0
+    finally:
+        sq.lib().sq_debug_inject(0)
+        sq.set_wait_timeout_ns(0)
+
+
 def test_python_checks():
     q, sf = _buffers(4, 64, MX)
     x = torch.zeros(4, 64, device="cuda")

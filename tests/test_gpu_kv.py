@@ -279,6 +279,30 @@ def test_decode_steps_in_a_graph(fmt):
         assert torch.all(ko[B * (i + 1):] == 7.0)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_extremes(fmt):
+    """Rows of subnormal numbers, of the least and the largest normal ones, of one element beside zeros."""
+    D = 64
+    x = np.zeros((9, 1, D), np.float32)
+    x[0] = np.ldexp(np.float32(1.3), np.linspace(-149, -127, D).astype(int))
+    x[1] = 1e-45
+    x[2] = np.linspace(-190, 190, D).astype(np.float32) * np.float32(2.0 ** -149)
+    x[3] = np.linspace(-1, 1, D).astype(np.float32) * np.float32(2.0 ** -121)
+    x[4] = np.linspace(-1, 1, D).astype(np.float32) * np.float32(2.0 ** -126)
+    x[5] = np.finfo(np.float32).max * np.linspace(-1, 1, D).astype(np.float32)
+    x[6, 0, 63] = -7.25
+    x[7, 0, 0], x[7, 0, 1] = -0.0, 3e38
+    x[8] = np.ldexp(np.float32(-1.9), np.linspace(-149, 127, D).astype(int))
+    cache = _cache(9, 1, 1, D, fmt)
+    sq.kv_cache_write(dev(x), dev(x), dev(np.arange(9)), fmt, *cache)
+    ko, vo = (torch.empty(9, 1, D, device="cuda") for _ in "kv")
+    sq.kv_cache_read(fmt, *cache, dev(np.arange(9, dtype=np.int32)[None]), dev(np.array([0, 9], np.int32)), ko, vo)
+    _sync()
+    rows, sc, val = _oracle_rows(x, fmt, F32)
+    assert np.array_equal(_bytes(cache[0]), rows) and np.array_equal(_bytes(cache[1]), sc)
+    assert np.array_equal(host(ko), val) and np.array_equal(host(vo), val)
+
+
 def test_python_checks():
     fmt = sq.KV_INT8
     c = _cache(2, 4, 3, 64, fmt)

@@ -14,14 +14,10 @@ enum DType : int { DT_F32 = 0, DT_F16 = 1, DT_BF16 = 2 };
 
 __host__ __device__ constexpr int dtype_size(int dt) { return dt == DT_F32 ? 4 : 2; }
 
-// First error code (a barrier timeout, a bad index) recorded by any kernel of
-// this translation unit on this device (0 = none).  Read and cleared by
-// sq_sync_status, which takes every translation unit's word.
+// First barrier-timeout code recorded by any kernel of this translation unit on
+// this device (0 = none).  Read and cleared by sq_sync_status, which takes every
+// translation unit's word.
 static __device__ unsigned int g_error_word;
-
-// Codes from here on record an index of the caller that lies outside its
-// tensor (the access was skipped); those below are barrier timeouts.
-constexpr unsigned ERR_BAD_INDEX = 0x200;
 
 // Programmatic dependent launch.  On created streams every kernel of this
 // library is launched with programmatic stream serialisation and executes

@@ -6,6 +6,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 #include <unordered_map>
@@ -219,7 +220,9 @@ inline bool make_out_map(CUtensorMap *m, void *base, int out_dt, bool s32, int64
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // Each translation unit has its own device error word (common.cuh); this
-// reads and clears the current device's word of libsq_fp4.cu.
-cudaError_t fp4_error_word_take(unsigned int *word);
+// reads and clears the current device's words of libsq_fp4.cu: the barrier
+// timeout and the key/value cache's bad index.
+cudaError_t fp4_error_words_take(unsigned int *timeout, unsigned int *bad_index);
+inline std::atomic<bool> g_fp4_launched{false};   // a call that can set one of them was made
 
 }  // namespace sq

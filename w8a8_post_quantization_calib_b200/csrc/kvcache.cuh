@@ -40,7 +40,11 @@ __host__ __device__ constexpr int row_bytes(int fmt, int D)
 }
 __host__ __device__ constexpr int scale_bytes(int fmt, int D) { return fmt == KV_MXFP4 ? (D + 31) / 32 : 4; }
 
-__device__ __forceinline__ void bad_index() { atomicCAS(&g_error_word, 0u, ERR_BAD_INDEX); }
+// 1 once a kernel met an index of the caller outside the cache (the access was
+// skipped).  Apart from g_error_word, so that it hides no barrier timeout.
+static __device__ unsigned int g_bad_index;
+
+__device__ __forceinline__ void bad_index() { atomicExch(&g_bad_index, 1u); }
 
 struct WriteArgs {
     const void *k, *v;         // [T, H, D], tokens k_ld / v_ld elements apart

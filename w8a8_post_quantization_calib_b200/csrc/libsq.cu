@@ -555,18 +555,19 @@ sq_status sq_sync_status(sq_stream stream)
 {
     cudaError_t e = cudaStreamSynchronize(as_stream(stream));
     if (e != cudaSuccess) return cuda_fail(e);
-    unsigned int word = 0, word4 = 0;
+    unsigned int word = 0, word4 = 0, bad_index = 0;
     e = cudaMemcpyFromSymbol(&word, g_error_word, sizeof(word));
     if (e != cudaSuccess) return cuda_fail(e);
     if (word != 0) {
         const unsigned int zero = 0;
         cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero));
     }
-    e = fp4_error_word_take(&word4);
-    if (e != cudaSuccess) return cuda_fail(e);
-    if (word != 0) return SQ_ERR_TIMEOUT;
-    if (word4 != 0) return word4 >= ERR_BAD_INDEX ? SQ_ERR_INVALID_ARG : SQ_ERR_TIMEOUT;
-    return SQ_OK;
+    if (g_fp4_launched.load()) {
+        e = fp4_error_words_take(&word4, &bad_index);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    if (word != 0 || word4 != 0) return SQ_ERR_TIMEOUT;
+    return bad_index != 0 ? SQ_ERR_INVALID_ARG : SQ_OK;
 }
 
 sq_status sq_calib_absmax(const void *x, sq_dtype dt, int64_t rows, int64_t cols, int64_t ld, float *absmax,

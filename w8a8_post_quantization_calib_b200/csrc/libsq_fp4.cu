@@ -15,13 +15,14 @@ using namespace sq;
 
 namespace sq {
 
-cudaError_t fp4_error_word_take(unsigned int *word)
+cudaError_t fp4_error_words_take(unsigned int *timeout, unsigned int *bad_index)
 {
-    *word = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(word, g_error_word, sizeof(*word));
-    if (e != cudaSuccess || *word == 0) return e;
     const unsigned int zero = 0;
-    return cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero));
+    cudaError_t e = cudaMemcpyFromSymbol(timeout, g_error_word, sizeof(*timeout));
+    if (e == cudaSuccess && *timeout != 0) e = cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero));
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(bad_index, kv::g_bad_index, sizeof(*bad_index));
+    if (e == cudaSuccess && *bad_index != 0) e = cudaMemcpyToSymbol(kv::g_bad_index, &zero, sizeof(zero));
+    return e;
 }
 
 }  // namespace sq
@@ -459,6 +460,7 @@ sq_status sq_linear_fp4(const uint8_t *xq4, const uint8_t *x_sf, const uint8_t *
     p.out_dt = out_dt;
     fp.g_act = fmt == SQ_NVFP4 ? g_act : nullptr;
     fp.g_w = fmt == SQ_NVFP4 ? g_w : nullptr;
+    g_fp4_launched.store(true);
     const Fp4Operands o{xq4, x_sf, wq4, w_sf, fp4::code_row_bytes(K), fp4::scale_tiles_k(fmt, K)};
     const cudaStream_t st = as_stream(stream);
     return fmt == SQ_MXFP4 ? dispatch_fp4<fp4::FMT_MX>(fp, o, st) : dispatch_fp4<fp4::FMT_NV>(fp, o, st);
@@ -493,6 +495,7 @@ sq_status sq_kv_cache_write(const void *k, const void *v, sq_dtype dt, int64_t T
         (reinterpret_cast<uintptr_t>(slots) & 7) != 0)
         return SQ_ERR_MISALIGNED;
     const int ll = lanes_log2(static_cast<int>(D));
+    g_fp4_launched.store(true);
     kv::WriteArgs a{k, v, T, k_ld, v_ld, num_slots, slots, static_cast<uint8_t *>(k_cache),
                     static_cast<uint8_t *>(v_cache), k_scale, v_scale, static_cast<int>(H), static_cast<int>(D), ll, 0,
                     inverse63(H)};
@@ -537,6 +540,7 @@ sq_status sq_kv_cache_read(sq_kv_format fmt, const void *k_cache, const void *k_
           reinterpret_cast<uintptr_t>(starts)) & 3) != 0)
         return SQ_ERR_MISALIGNED;
     const int ll = lanes_log2(static_cast<int>(D));
+    g_fp4_launched.store(true);
     kv::ReadArgs a{static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), k_scale, v_scale,
                    num_pages, max_pages, table, cu_rows, starts, total, k_out, v_out, static_cast<int>(B),
                    static_cast<int>(H), static_cast<int>(D), static_cast<int>(cdiv(H, 32 >> ll)),
