@@ -367,19 +367,24 @@ __device__ __forceinline__ void store_strip(uint8_t *stage, uint8_t *strip, int6
 
 // ---------------------------------------------------------------------------
 // Rows and columns of a block of 32 x 8 threads: a warp covers 512 columns (16
-// a lane: an NVFP4 block, half an MXFP4 block), a thread the four rows r, r +
-// 32, r + 64, r + 96 of a 128-row scale tile, whose scale words lie in 16
-// contiguous bytes.  A unit is eight such r; a block walks units, so that its
-// columns' smoothing constants stay in registers.
+// a lane: an NVFP4 block, half an MXFP4 block), a thread ROWS rows.  ROWS = 4: r,
+// r + 32, r + 64, r + 96 of a 128-row scale tile, whose scale words lie in 16
+// contiguous bytes; a unit is eight such r.  ROWS = 1 (a unit is eight rows) where
+// that would leave SMs idle.  A block walks units, so that its columns'
+// smoothing constants stay in registers.
 // ---------------------------------------------------------------------------
-constexpr int QTX = 32, QTY = 8, QROWS = 4;
+constexpr int QTX = 32, QTY = 8;
 
-__host__ __device__ constexpr int64_t quant_units(int64_t rows)
+template <int ROWS> __host__ __device__ constexpr int64_t quant_units(int64_t rows)
 {
+    if (ROWS == 1) return (rows + QTY - 1) / QTY;
     const int64_t last = rows & 127;                        // the last tile's units with at least one row
     return (rows >> 7) * 4 + (last >= 32 ? 4 : (last + QTY - 1) / QTY);
 }
-__device__ __forceinline__ int64_t unit_row(int64_t unit, int ty) { return (unit >> 2) * 128 + (unit & 3) * QTY + ty; }
+template <int ROWS> __device__ __forceinline__ int64_t unit_row(int64_t unit, int ty)
+{
+    return ROWS == 1 ? unit * QTY + ty : (unit >> 2) * 128 + (unit & 3) * QTY + ty;
+}
 
 // ---------------------------------------------------------------------------
 // Quantisation.  Bound by memory: [16384, 8192] bf16 -> MXFP4 reads and writes
@@ -399,11 +404,11 @@ struct QuantArgs {
     int weight;                // multiply with s_j instead of recip(s_j)
 };
 
-template <int DT, int VEC>
-__device__ __forceinline__ void load_rows(const QuantArgs &a, int64_t r, int64_t c, Raw16<DT> (&raw)[QROWS])
+template <int DT, int VEC, int ROWS>
+__device__ __forceinline__ void load_rows(const QuantArgs &a, int64_t r, int64_t c, Raw16<DT> (&raw)[ROWS])
 {
 #pragma unroll
-    for (int u = 0; u < QROWS; ++u) {
+    for (int u = 0; u < ROWS; ++u) {
         if (r + 32 * u >= a.rows) break;
         const uint8_t *row = static_cast<const uint8_t *>(a.x) + (r + 32 * u) * a.ld * dtype_size(DT);
         if constexpr (VEC >= 16) {
@@ -416,7 +421,7 @@ __device__ __forceinline__ void load_rows(const QuantArgs &a, int64_t r, int64_t
     }
 }
 
-template <int DT, int VEC, int FMT>
+template <int DT, int VEC, int FMT, int ROWS>
 __global__ void __launch_bounds__(QTX *QTY) k_fp4_quant(const QuantArgs a)
 {
     constexpr int TILE_K = FmtT<FMT>::TILE_K;
@@ -427,8 +432,8 @@ __global__ void __launch_bounds__(QTX *QTY) k_fp4_quant(const QuantArgs a)
     const int64_t c = (static_cast<int64_t>(blockIdx.x) * QTX + lane) * 16;
     const int64_t ktiles = scale_tiles_k(FMT, a.K), qld = code_row_bytes(a.K);
     pdl_wait();
-    Raw16<DT> raw[QROWS];
-    load_rows<DT, VEC>(a, unit_row(blockIdx.y, threadIdx.y), c, raw);
+    Raw16<DT> raw[ROWS];
+    load_rows<DT, VEC, ROWS>(a, unit_row<ROWS>(blockIdx.y, threadIdx.y), c, raw);
     // each factor once a block (a reciprocal costs more than the rest of a column)
     for (int i = threadIdx.y * QTX + lane; i < 16 * QTX; i += QTX * QTY) {
         const int64_t col = static_cast<int64_t>(blockIdx.x) * (16 * QTX) + i;
@@ -454,13 +459,13 @@ __global__ void __launch_bounds__(QTX *QTY) k_fp4_quant(const QuantArgs a)
     const int64_t kt = c / TILE_K;
     const int j = (lane / LB) & 3;                          // this lane's block in its scale tile
     for (int64_t unit = blockIdx.y; unit < a.units; unit += gridDim.y) {
-        const int64_t r = unit_row(unit, threadIdx.y);
-        Raw16<DT> next[QROWS];                              // the next unit's loads run while this one is computed
-        if (unit + gridDim.y < a.units) load_rows<DT, VEC>(a, unit_row(unit + gridDim.y, threadIdx.y), c, next);
+        const int64_t r = unit_row<ROWS>(unit, threadIdx.y);
+        Raw16<DT> next[ROWS];                              // the next unit's loads run while this one is computed
+        if (unit + gridDim.y < a.units) load_rows<DT, VEC, ROWS>(a, unit_row<ROWS>(unit + gridDim.y, threadIdx.y), c, next);
         if (r < a.rows) {                                   // the same for the whole warp
-            uint32_t bytes = 0;                             // the four rows' scales of this block
+            uint32_t bytes = 0;                             // the rows' scales of this block
 #pragma unroll
-            for (int u = 0; u < QROWS; ++u) {
+            for (int u = 0; u < ROWS; ++u) {
                 const int64_t row = r + 32 * u;
                 if (row >= a.rows) break;
                 float f[16];
@@ -486,17 +491,24 @@ __global__ void __launch_bounds__(QTX *QTY) k_fp4_quant(const QuantArgs a)
                 if (c < 2 * qld)
                     *reinterpret_cast<uint2 *>(a.q + row * qld + (c >> 1)) = make_uint2(e2m1x8(f), e2m1x8(f + 8));
             }
-            // 4 x 4 bytes transposed over the four lanes of a scale tile: lane
-            // j gets the word of row r + 32 j
-            uint32_t t = __shfl_xor_sync(0xffffffffu, bytes, LB);
-            bytes = __byte_perm(bytes, t, (j & 1) ? 0x3715 : 0x6240);
-            t = __shfl_xor_sync(0xffffffffu, bytes, 2 * LB);
-            bytes = __byte_perm(bytes, t, (j & 2) ? 0x3276 : 0x5410);
-            if (lane % LB == 0 && kt < ktiles && r + 32 * j < a.rows)
-                *reinterpret_cast<uint32_t *>(a.sf + scale_word(r, kt, ktiles) + 4 * j) = bytes;
+            if constexpr (ROWS == 4) {
+                // 4 x 4 bytes transposed over the four lanes of a scale tile:
+                // lane j gets the word of row r + 32 j
+                uint32_t t = __shfl_xor_sync(0xffffffffu, bytes, LB);
+                bytes = __byte_perm(bytes, t, (j & 1) ? 0x3715 : 0x6240);
+                t = __shfl_xor_sync(0xffffffffu, bytes, 2 * LB);
+                bytes = __byte_perm(bytes, t, (j & 2) ? 0x3276 : 0x5410);
+                if (lane % LB == 0 && kt < ktiles && r + 32 * j < a.rows)
+                    *reinterpret_cast<uint32_t *>(a.sf + scale_word(r, kt, ktiles) + 4 * j) = bytes;
+            } else {
+                bytes <<= 8 * j;
+                bytes |= __shfl_xor_sync(0xffffffffu, bytes, LB);
+                bytes |= __shfl_xor_sync(0xffffffffu, bytes, 2 * LB);
+                if (lane % (4 * LB) == 0 && kt < ktiles) *reinterpret_cast<uint32_t *>(a.sf + scale_word(r, kt, ktiles)) = bytes;
+            }
         }
 #pragma unroll
-        for (int u = 0; u < QROWS; ++u) raw[u] = next[u];
+        for (int u = 0; u < ROWS; ++u) raw[u] = next[u];
     }
     __syncthreads();
     pdl_trigger();
@@ -515,7 +527,7 @@ struct DequantArgs {
     int64_t units;
 };
 
-template <int DT, int VEC, int FMT>
+template <int DT, int VEC, int FMT, int ROWS>
 __global__ void __launch_bounds__(QTX *QTY) k_fp4_dequant(const DequantArgs a)
 {
     constexpr int TILE_K = FmtT<FMT>::TILE_K, SZ = dtype_size(DT);
@@ -528,27 +540,38 @@ __global__ void __launch_bounds__(QTX *QTY) k_fp4_dequant(const DequantArgs a)
     if (VEC < 16 || in) {                                   // narrow stores take the whole warp
         const int64_t kt = c / TILE_K;
         const int shift = 8 * (static_cast<int>(c % TILE_K) / FmtT<FMT>::BLOCK);
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);               // the four rows' scale words (inside the tile, used or not)
-        uint2 next[QROWS] = {};
+        uint32_t words_next[ROWS] = {};                     // the rows' scale words (inside the tile, used or not)
+        uint2 next[ROWS] = {};
         auto load = [&](int64_t unit) {
-            const int64_t r = unit_row(unit, threadIdx.y);
+            const int64_t r = unit_row<ROWS>(unit, threadIdx.y);
             if (unit >= a.units || r >= a.rows || !in) return;
-            w = __ldg(reinterpret_cast<const uint4 *>(a.sf + scale_word(r, kt, ktiles)));
+            if constexpr (ROWS == 4) {
+                const uint4 w = __ldg(reinterpret_cast<const uint4 *>(a.sf + scale_word(r, kt, ktiles)));
+                words_next[0] = w.x;
+                words_next[1] = w.y;
+                words_next[2] = w.z;
+                words_next[3] = w.w;
+            } else {
+                words_next[0] = __ldg(reinterpret_cast<const uint32_t *>(a.sf + scale_word(r, kt, ktiles)));
+            }
 #pragma unroll
-            for (int u = 0; u < QROWS; ++u)
+            for (int u = 0; u < ROWS; ++u)
                 if (r + 32 * u < a.rows) next[u] = __ldg(reinterpret_cast<const uint2 *>(a.q + (r + 32 * u) * qld + (c >> 1)));
         };
         load(blockIdx.y);
         for (int64_t unit = blockIdx.y; unit < a.units; unit += gridDim.y) {
-            const int64_t r = unit_row(unit, threadIdx.y);
-            const uint32_t words[QROWS] = {w.x, w.y, w.z, w.w};
-            uint2 q[QROWS];
+            const int64_t r = unit_row<ROWS>(unit, threadIdx.y);
+            uint32_t words[ROWS];
+            uint2 q[ROWS];
 #pragma unroll
-            for (int u = 0; u < QROWS; ++u) q[u] = next[u];
+            for (int u = 0; u < ROWS; ++u) {
+                words[u] = words_next[u];
+                q[u] = next[u];
+            }
             load(unit + gridDim.y);                         // runs while this unit is computed
             if (r >= a.rows) continue;
 #pragma unroll
-            for (int u = 0; u < QROWS; ++u) {
+            for (int u = 0; u < ROWS; ++u) {
                 const int64_t row = r + 32 * u;
                 if (row >= a.rows) break;
                 const uint32_t b = (words[u] >> shift) & 0xffu;

@@ -12,11 +12,11 @@
 // fp4.cuh) comes into shared memory by TMA and takes 4 TMEM columns (row r at
 // lane r % 32, column r / 32, replicated to the four lane quarters).
 //
-//   k_fp4_swap (M <= 128): the weights fill the 128-row MMA and stream once;
-//     a cluster of CS CTAs shares a tile's K range where tiles are few.
+//   k_fp4_swap (M <= 128, or few tiles): the weights fill the 128-row MMA; a
+//     cluster of CS CTAs shares a tile's K range.
 //     Scales go to TMEM by tcgen05.cp: issued by the MMA's thread, executed in
 //     order with the MMAs, no barrier.  Roles and barriers are gemm.cuh's.
-//   k_fp4_pair (M > 128): CTA pairs (cta_group::2), 256 x BN tiles.  Each CTA
+//   k_fp4_pair: CTA pairs (cta_group::2), 256 x BN tiles.  Each CTA
 //     loads its 128 rows of A and BN/2 rows of B, its rows' A scales and all
 //     BN rows' B scales (each SM scales its own 128 x BN accumulator).  Four
 //     more warps bring the scales from their own shared-memory ring to TMEM
@@ -119,6 +119,12 @@ __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr)
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr)
 {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc_scales(saddr)) : "memory");
+}
+
+// This lane's 16 bytes of a scale tile in shared memory.
+__device__ __forceinline__ void load_scale_words(uint32_t *d, uint32_t a)
+{
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "r"(a) : "memory");
 }
 
 // N words (4, 8 or 16) of this thread's TMEM lane from registers.
@@ -842,18 +848,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
                 if (!ok) break;
                 const uint32_t ssa = sf_base + slot * C::SF_BYTES + lane * 16, ssb = ssa + C::SFA_BYTES;
                 uint32_t r[C::SF_COLS];
-                auto word4 = [](uint32_t *d, uint32_t a) {
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
-                                 : "r"(a)
-                                 : "memory");
-                };
 #pragma unroll
                 for (int i = 0; i < KBO * Sf::TILES; ++i) {
-                    word4(r + 4 * i, ssa + i * SF_TILE);
+                    load_scale_words(r + 4 * i, ssa + i * SF_TILE);
 #pragma unroll
                     for (int t = 0; t < C::NB; ++t)
-                        word4(r + C::SFA_COLS + 4 * (i * C::NB + t), ssb + (t * KBO * Sf::TILES + i) * SF_TILE);
+                        load_scale_words(r + C::SFA_COLS + 4 * (i * C::NB + t), ssb + (t * KBO * Sf::TILES + i) * SF_TILE);
                 }
                 if (n >= C::SF_BUFS) {         // the MMAs that read this buffer have completed
                     ok = wait(empty_bar(old), ophase, ERR_MMA + 5);
