@@ -71,10 +71,10 @@ def test_quant(rows, K, dt, fmt, weight):
 
 @pytest.mark.parametrize("fmt", [MX, NV])
 @pytest.mark.parametrize("dt", [F32, F16, BF16])
-@pytest.mark.parametrize("pad,off", [(24, 0), (7, 0), (5, 3), (16, 8)])
-def test_quant_rows_of_a_wider_tensor(fmt, dt, pad, off):
+@pytest.mark.parametrize("pad,off", [(24, 0), (7, 0), (5, 3), (16, 8), (1, 0), (1, 1), (2, 2), (3, 1), (4, 4), (6, 5), (9, 7)])
+@pytest.mark.parametrize("rows,K", [(70, 600), (1, 517), (3, 15), (40, 1025)])
+def test_quant_rows_of_a_wider_tensor(fmt, dt, pad, off, rows, K):
     """Any row stride and any start: the loads narrow to what the addresses allow; no s, no g."""
-    rows, K = 70, 600
     x = rand_x(pad + off, (rows, K + pad), dt, 1.0)
     q, sf = _buffers(rows, K, fmt)
     sq.smooth_quant_act_fp4(dev(x, dt)[:, off:off + K], None, fmt, q, sf)
@@ -147,6 +147,22 @@ def test_dequant(rows, K, dt, fmt):
     want = torch.from_numpy(v.copy()).to(TORCH_DT[dt])
     assert torch.equal(torch.nan_to_num(out[:rows].cpu(), nan=777.0), torch.nan_to_num(want, nan=777.0))
     assert torch.all(out[rows] == 7.0)
+
+
+@pytest.mark.parametrize("off", range(8))
+@pytest.mark.parametrize("rows,K", [(1, 1), (3, 515), (9, 1027), (5, 511), (2, 1024), (33, 17)])
+@pytest.mark.parametrize("dt", [F32, F16, BF16])
+def test_dequant_to_any_address(off, rows, K, dt):
+    """Outputs that start and whose rows end anywhere; what lies around them stays."""
+    r = np.random.default_rng(off + K)
+    n = -(-K // 32) * 32 // 16
+    codes, sb = r.integers(0, 16, (rows, n * 16)), r.integers(1, 100, (rows, n)).astype(np.uint8)
+    full = torch.full((rows * K + 32,), 7.0, dtype=TORCH_DT[dt], device="cuda")
+    sq.dequant_fp4(dev(oracle.fp4_pack(codes)), dev(oracle.fp4_tile_scales(sb, 0xEE)), NV, full[off:off + rows * K].view(rows, K))
+    _sync()
+    want = torch.full(full.shape, 7.0, dtype=TORCH_DT[dt])
+    want[off:off + rows * K] = torch.from_numpy(oracle.fp4_values(codes, sb, NV)[:, :K].copy()).flatten().to(TORCH_DT[dt])
+    assert torch.equal(full.cpu(), want)
 
 
 # ------------------------------------------------------------------ product

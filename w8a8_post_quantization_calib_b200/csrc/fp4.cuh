@@ -235,16 +235,12 @@ __device__ __forceinline__ void widen16(const Raw16<DT> &r, float (&f)[16])
     }
 }
 
-// 16 values of a row at column c, rounded to the output type; those at n and
-// behind are not stored.  VEC as in load16.
-template <int DT, int VEC>
-__device__ __forceinline__ void store16(void *row, int64_t c, int64_t n, const float (&f)[16])
+// 16 values rounded to the output type, as words
+template <int DT>
+__device__ __forceinline__ void round16(const float (&f)[16], uint32_t (&w)[4 * dtype_size(DT)])
 {
-    constexpr int SZ = dtype_size(DT), NV = SZ;
-    uint8_t *p = static_cast<uint8_t *>(row) + c * SZ;
-    uint32_t w[4 * NV];
 #pragma unroll
-    for (int i = 0; i < 4 * NV; ++i) {
+    for (int i = 0; i < 4 * dtype_size(DT); ++i) {
         if constexpr (DT == DT_F32) {
             w[i] = __float_as_uint(f[i]);
         } else if constexpr (DT == DT_F16) {
@@ -255,6 +251,17 @@ __device__ __forceinline__ void store16(void *row, int64_t c, int64_t n, const f
             w[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
     }
+}
+
+// 16 values of a row at column c, rounded to the output type; those at n and
+// behind are not stored.  VEC as in load16.
+template <int DT, int VEC>
+__device__ __forceinline__ void store16(void *row, int64_t c, int64_t n, const float (&f)[16])
+{
+    constexpr int SZ = dtype_size(DT), NV = SZ;
+    uint8_t *p = static_cast<uint8_t *>(row) + c * SZ;
+    uint32_t w[4 * NV];
+    round16<DT>(f, w);
     constexpr int PV = VEC == 32 ? 16 : VEC < SZ ? 0 : VEC;
     if (VEC == 32 && c + 16 <= n) {
 #pragma unroll
@@ -297,72 +304,130 @@ __device__ __forceinline__ void store16_rt(int vec, void *row, int64_t c, int64_
     else store16<DT, 0>(row, c, n, f);
 }
 
-// Rows that allow accesses of 4 or 2 bytes only (PB): a warp takes the 512
-// columns of its strip in pieces 32 lanes apart, which coalesce, and hands each
-// lane its 16 neighbouring columns through shared memory (`stage`, 512 elements
-// of the warp).  left: bytes of the row from the strip's start on.
-template <int DT> constexpr int strip_bytes() { return 512 * dtype_size(DT); }
+// Rows off 16 bytes.  A lane's 16 elements are loaded as the 16-byte vectors
+// around them, one more than they take, and moved into place in registers; they
+// are stored the other way round, with the end of the lane before in front.
+// Loads may take bytes beside the row, but none outside [lo, hi), the tensor.
 
-template <int DT, int PB>
-__device__ __forceinline__ void load_strip(const uint8_t *strip, int64_t left, int lane, Raw16<DT> &r)
+// words [0, N - 4) of the result start `bytes` (even, below 16) behind ext[0]
+template <int N>
+__device__ __forceinline__ void shift_words(uint32_t (&ext)[N], int bytes)
 {
-    constexpr int WORDS = 4 * dtype_size(DT);
-    uint32_t w[WORDS];
-    auto half = [&](int64_t o) {
-        return o + 2 <= left ? static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(strip + o))) : 0u;
-    };
+    if (bytes & 8) {
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) {
-        if constexpr (PB == 4) {
-            const int64_t o = (i * 32 + lane) * 4;
-            w[i] = o + 4 <= left ? __ldg(reinterpret_cast<const uint32_t *>(strip + o)) : dtype_size(DT) == 2 ? half(o) : 0u;
-        } else {
-            w[i] = half((2 * i * 32 + lane) * 2) | (half(((2 * i + 1) * 32 + lane) * 2) << 16);
-        }
+        for (int i = 0; i < N - 2; ++i) ext[i] = ext[i + 2];
     }
+    if (bytes & 4) {
 #pragma unroll
-    for (int i = 0; i < dtype_size(DT); ++i) r.v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        for (int i = 0; i < N - 1; ++i) ext[i] = ext[i + 1];
+    }
+    if (bytes & 2) {
+#pragma unroll
+        for (int i = 0; i < N - 1; ++i) ext[i] = __funnelshift_r(ext[i], ext[i + 1], 16);
+    }
 }
 
-template <int DT, int PB>
-__device__ __forceinline__ void pieces_to_columns(uint8_t *stage, int lane, Raw16<DT> &r)
+template <int DT> struct Around16 { uint32_t w[4 * dtype_size(DT) + 4]; };
+
+// The vectors around elements [c, c + 16) of the row; n: the row's elements.
+template <int DT>
+__device__ __forceinline__ void load_around(const uint8_t *row, int64_t c, int64_t n, const uint8_t *lo, const uint8_t *hi,
+                                            Around16<DT> &r)
 {
     constexpr int SZ = dtype_size(DT);
+    const uint8_t *a = row + c * SZ;
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(a) & 15);
+    const uint8_t *p = a - off;
+    const uint8_t *end = row + n * SZ;                      // vectors from here on hold nothing of the row
 #pragma unroll
-    for (int i = 0; i < SZ; ++i) {
-        const uint32_t w[4] = {r.v[i].x, r.v[i].y, r.v[i].z, r.v[i].w};
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int k = 4 * i + t;
-            if constexpr (PB == 4) {
-                reinterpret_cast<uint32_t *>(stage)[k * 32 + lane] = w[t];
+    for (int i = 0; i < SZ + 1; ++i, p += 16) {
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (p < end && (i < SZ || off != 0)) {
+            if (p >= lo && p + 16 <= hi) {
+                load_words<16>(p, w);
             } else {
-                reinterpret_cast<uint16_t *>(stage)[2 * k * 32 + lane] = static_cast<uint16_t>(w[t]);
-                reinterpret_cast<uint16_t *>(stage)[(2 * k + 1) * 32 + lane] = static_cast<uint16_t>(w[t] >> 16);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint8_t *e = p + 2 * j;
+                    if (e >= lo && e < hi) w[j / 2] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(e))) << (16 * (j & 1));
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r.w[4 * i + j] = w[j];
+    }
+}
+
+// Elements [c, c + 16) of the row out of the vectors around them; 0 at n and behind.
+template <int DT>
+__device__ __forceinline__ void settle(const uint8_t *row, int64_t c, int64_t n, Around16<DT> &r, Raw16<DT> &out)
+{
+    constexpr int SZ = dtype_size(DT);
+    shift_words(r.w, static_cast<int>(reinterpret_cast<uintptr_t>(row + c * SZ) & 15));
+    if (c + 16 > n) {
+#pragma unroll
+        for (int i = 0; i < 4 * SZ; ++i) {
+            if constexpr (SZ == 4) {
+                if (c + i >= n) r.w[i] = 0u;
+            } else {
+                if (c + 2 * i >= n) r.w[i] = 0u;
+                else if (c + 2 * i + 1 >= n) r.w[i] &= 0xffffu;
             }
         }
     }
-    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < SZ; ++i) r.v[i] = reinterpret_cast<const uint4 *>(stage + lane * 16 * SZ)[i];
-    __syncwarp();
+    for (int i = 0; i < SZ; ++i) out.v[i] = make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
 }
 
-// The reverse: each lane's 16 rounded values leave in coalesced pieces.
-template <int DT, int PB>
-__device__ __forceinline__ void store_strip(uint8_t *stage, uint8_t *strip, int64_t left, int lane, const float (&f)[16])
+// 512 values of a strip (16 a lane, `left` elements of the row from its start
+// on) to any address of their type; the whole warp.
+template <int DT>
+__device__ __forceinline__ void store_strip(uint8_t *strip, int64_t left, int lane, const float (&f)[16])
 {
-    constexpr int WORDS = 4 * dtype_size(DT);
-    store16<DT, 16>(stage, lane * 16, 512, f);
-    __syncwarp();
+    constexpr int SZ = dtype_size(DT), N = 4 * SZ;
+    uint32_t w[N];
+    round16<DT>(f, w);
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(strip) & 15);
+    uint32_t ext[N + 4];
 #pragma unroll
-    for (int i = 0; i < (PB == 4 ? WORDS : 2 * WORDS); ++i) {
-        const int o = (i * 32 + lane) * PB;
-        if (PB == 4 && o + 4 <= left) *reinterpret_cast<uint32_t *>(strip + o) = *reinterpret_cast<const uint32_t *>(stage + o);
-        else if (dtype_size(DT) == 2 && o + 2 <= left)
-            *reinterpret_cast<uint16_t *>(strip + o) = *reinterpret_cast<const uint16_t *>(stage + o);
+    for (int i = 0; i < 4; ++i) ext[i] = __shfl_up_sync(0xffffffffu, w[N - 4 + i], 1);
+#pragma unroll
+    for (int i = 0; i < N; ++i) ext[4 + i] = w[i];
+    const int64_t bytes = left * SZ;
+    if (off == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) ext[i] = w[i];
+    } else {
+        shift_words(ext, 16 - off);
     }
-    __syncwarp();
+    // this lane's vectors: bytes o .. o + 15 of the strip
+#pragma unroll
+    for (int i = 0; i < SZ; ++i) {
+        const int o = lane * 16 * SZ + 16 * i - off;
+        if (o >= 0 && o + 16 <= bytes) {
+            store_words<16>(strip + o, ext + 4 * i);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16 / SZ; ++j) {
+                const int e = o + j * SZ;
+                if (e >= 0 && e < bytes) {
+                    if constexpr (SZ == 4) *reinterpret_cast<uint32_t *>(strip + e) = ext[4 * i + j];
+                    else *reinterpret_cast<uint16_t *>(strip + e) = static_cast<uint16_t>(ext[4 * i + j / 2] >> (16 * (j & 1)));
+                }
+            }
+        }
+    }
+    // the strip's last `off` bytes lie behind the last lane's vectors
+    if (lane == 31 && off != 0) {
+#pragma unroll
+        for (int j = 0; j < 16 / SZ; ++j) {
+            const int e = 512 * SZ - 16 + j * SZ;
+            if (e >= 512 * SZ - off && e < bytes) {
+                if constexpr (SZ == 4) *reinterpret_cast<uint32_t *>(strip + e) = w[N - 4 + j];
+                else *reinterpret_cast<uint16_t *>(strip + e) = static_cast<uint16_t>(w[N - 4 + j / 2] >> (16 * (j & 1)));
+            }
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -404,20 +469,21 @@ struct QuantArgs {
     int weight;                // multiply with s_j instead of recip(s_j)
 };
 
+// A row's 16 elements on their way: VEC 32 or 16, or (0) rows off 16 bytes.
+template <int DT, int VEC> struct InFlight { Raw16<DT> v; };
+template <int DT> struct InFlight<DT, 0> { Around16<DT> v; };
+
 template <int DT, int VEC, int ROWS>
-__device__ __forceinline__ void load_rows(const QuantArgs &a, int64_t r, int64_t c, Raw16<DT> (&raw)[ROWS])
+__device__ __forceinline__ void load_rows(const QuantArgs &a, int64_t r, int64_t c, InFlight<DT, VEC> (&raw)[ROWS])
 {
+    constexpr int SZ = dtype_size(DT);
+    const uint8_t *x = static_cast<const uint8_t *>(a.x);
 #pragma unroll
     for (int u = 0; u < ROWS; ++u) {
         if (r + 32 * u >= a.rows) break;
-        const uint8_t *row = static_cast<const uint8_t *>(a.x) + (r + 32 * u) * a.ld * dtype_size(DT);
-        if constexpr (VEC >= 16) {
-            load16<DT, VEC>(row, c, a.K, raw[u]);
-        } else {
-            const int lane = threadIdx.x;
-            const int64_t c0 = c - lane * 16;               // the strip's first column
-            load_strip<DT, VEC>(row + c0 * dtype_size(DT), (a.K - c0) * dtype_size(DT), lane, raw[u]);
-        }
+        const uint8_t *row = x + (r + 32 * u) * a.ld * SZ;
+        if constexpr (VEC != 0) load16<DT, VEC>(row, c, a.K, raw[u].v);
+        else load_around<DT>(row, c, a.K, x, x + ((a.rows - 1) * a.ld + a.K) * SZ, raw[u].v);
     }
 }
 
@@ -427,12 +493,11 @@ __global__ void __launch_bounds__(QTX *QTY) k_fp4_quant(const QuantArgs a)
     constexpr int TILE_K = FmtT<FMT>::TILE_K;
     constexpr int LB = FMT == FMT_MX ? 2 : 1;               // lanes per block
     __shared__ float4 s_cs[4][QTX];                         // the strip's factors, [4 columns][lane]
-    __shared__ __align__(16) uint8_t s_stage[VEC < 16 ? QTY * strip_bytes<DT>() : 16];
     const int lane = threadIdx.x;
     const int64_t c = (static_cast<int64_t>(blockIdx.x) * QTX + lane) * 16;
     const int64_t ktiles = scale_tiles_k(FMT, a.K), qld = code_row_bytes(a.K);
     pdl_wait();
-    Raw16<DT> raw[ROWS];
+    InFlight<DT, VEC> raw[ROWS];
     load_rows<DT, VEC, ROWS>(a, unit_row<ROWS>(blockIdx.y, threadIdx.y), c, raw);
     // each factor once a block (a reciprocal costs more than the rest of a column)
     for (int i = threadIdx.y * QTX + lane; i < 16 * QTX; i += QTX * QTY) {
@@ -460,7 +525,7 @@ __global__ void __launch_bounds__(QTX *QTY) k_fp4_quant(const QuantArgs a)
     const int j = (lane / LB) & 3;                          // this lane's block in its scale tile
     for (int64_t unit = blockIdx.y; unit < a.units; unit += gridDim.y) {
         const int64_t r = unit_row<ROWS>(unit, threadIdx.y);
-        Raw16<DT> next[ROWS];                              // the next unit's loads run while this one is computed
+        InFlight<DT, VEC> next[ROWS];                      // the next unit's loads run while this one is computed
         if (unit + gridDim.y < a.units) load_rows<DT, VEC, ROWS>(a, unit_row<ROWS>(unit + gridDim.y, threadIdx.y), c, next);
         if (r < a.rows) {                                   // the same for the whole warp
             uint32_t bytes = 0;                             // the rows' scales of this block
@@ -469,8 +534,13 @@ __global__ void __launch_bounds__(QTX *QTY) k_fp4_quant(const QuantArgs a)
                 const int64_t row = r + 32 * u;
                 if (row >= a.rows) break;
                 float f[16];
-                if constexpr (VEC < 16) pieces_to_columns<DT, VEC>(s_stage + threadIdx.y * strip_bytes<DT>(), lane, raw[u]);
-                widen16<DT>(raw[u], f);
+                if constexpr (VEC != 0) {
+                    widen16<DT>(raw[u].v, f);
+                } else {
+                    Raw16<DT> x;
+                    settle<DT>(static_cast<const uint8_t *>(a.x) + row * a.ld * dtype_size(DT), c, a.K, raw[u].v, x);
+                    widen16<DT>(x, f);
+                }
                 float m = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
@@ -535,9 +605,8 @@ __global__ void __launch_bounds__(QTX *QTY) k_fp4_dequant(const DequantArgs a)
     const int64_t ktiles = scale_tiles_k(FMT, a.K), qld = code_row_bytes(a.K);
     pdl_wait();
     const float g = (FMT == FMT_NV && a.g != nullptr) ? __ldg(a.g) : 1.0f;
-    __shared__ __align__(16) uint8_t s_stage[VEC < 16 ? QTY * strip_bytes<DT>() : 16];
     const bool in = c < a.K;
-    if (VEC < 16 || in) {                                   // narrow stores take the whole warp
+    if (VEC == 0 || in) {                                   // rows off 16 bytes take the whole warp
         const int64_t kt = c / TILE_K;
         const int shift = 8 * (static_cast<int>(c % TILE_K) / FmtT<FMT>::BLOCK);
         uint32_t words_next[ROWS] = {};                     // the rows' scale words (inside the tile, used or not)
@@ -586,11 +655,11 @@ __global__ void __launch_bounds__(QTX *QTY) k_fp4_dequant(const DequantArgs a)
                     f[i + 1] = t.y;
                 }
                 uint8_t *out = static_cast<uint8_t *>(a.out) + row * a.K * SZ;
-                if constexpr (VEC >= 16) {
+                if constexpr (VEC != 0) {
                     store16<DT, VEC>(out, c, a.K, f);
                 } else {
                     const int64_t c0 = c - threadIdx.x * 16;
-                    store_strip<DT, VEC>(s_stage + threadIdx.y * strip_bytes<DT>(), out + c0 * SZ, (a.K - c0) * SZ, threadIdx.x, f);
+                    store_strip<DT>(out + c0 * SZ, a.K - c0, threadIdx.x, f);
                 }
             }
         }

@@ -54,7 +54,8 @@ inline dim3 strip_grid(int64_t units, int64_t cols, int per_sm)
 // One row a thread instead of four where four would give two thirds of the SMs
 // no block ([1021, 1000] bf16 -> NVFP4 3.9 -> 3.0 us, [200, 500] 4.2 -> 2.8; [1000,
 // 2048] 3.0 and 3.2), for fp32 rows, whose four take more registers, as long as
-// there are fewer than four blocks an SM ([2048, 4096] fp32 11.6 -> 8.5).
+// there are fewer than four blocks an SM ([2048, 4096] fp32 11.6 -> 8.5).  Rows
+// off 16 bytes (access width 0) always go one by one.
 inline bool few_units(int dt, int64_t rows, int64_t cols)
 {
     const int64_t blocks = fp4::quant_units<4>(rows) * cdiv(cols, 16 * fp4::QTX);
@@ -66,12 +67,15 @@ cudaError_t launch_quant(fp4::QuantArgs a, cudaStream_t st)
 {
     const int64_t cols = fp4::scale_tiles_k(FMT, a.K) * fp4::FmtT<FMT>::TILE_K;    // every byte of the scale tiles
     const dim3 block(fp4::QTX, fp4::QTY);
-    if (few_units(DT, a.rows, cols)) {
-        a.units = fp4::quant_units<1>(a.rows);
-        return launch_pdl(fp4::k_fp4_quant<DT, VEC, FMT, 1>, strip_grid(a.units, cols, QUANT_PER_SM), block, 0, st, a);
+    auto by_rows = [&](auto rows) {
+        constexpr int ROWS = decltype(rows)::value;
+        a.units = fp4::quant_units<ROWS>(a.rows);
+        return launch_pdl(fp4::k_fp4_quant<DT, VEC, FMT, ROWS>, strip_grid(a.units, cols, QUANT_PER_SM), block, 0, st, a);
+    };
+    if constexpr (VEC != 0) {
+        if (!few_units(DT, a.rows, cols)) return by_rows(std::integral_constant<int, 4>());
     }
-    a.units = fp4::quant_units<4>(a.rows);
-    return launch_pdl(fp4::k_fp4_quant<DT, VEC, FMT, 4>, strip_grid(a.units, cols, QUANT_PER_SM), block, 0, st, a);
+    return by_rows(std::integral_constant<int, 1>());
 }
 
 template <int DT, int VEC>
@@ -86,9 +90,7 @@ cudaError_t launch_quant_vec(const fp4::QuantArgs &a, int fmt, cudaStream_t st)
     const int vec = vec_bytes(a.x, a.ld * dtype_size(DT));
     if (vec == 32) return launch_quant_fmt<DT, 32>(a, fmt, st);
     if (vec == 16) return launch_quant_fmt<DT, 16>(a, fmt, st);
-    if (vec >= 4) return launch_quant_fmt<DT, 4>(a, fmt, st);
-    if constexpr (DT != DT_F32) return launch_quant_fmt<DT, 2>(a, fmt, st);
-    return cudaErrorInvalidValue;      // fp32 rows are 4-byte aligned
+    return launch_quant_fmt<DT, 0>(a, fmt, st);
 }
 
 sq_status quant_fp4(const void *x, int dt, int64_t rows, int64_t K, int64_t ld, const float *s, int weight, int fmt,
@@ -119,8 +121,10 @@ cudaError_t launch_dequant(fp4::DequantArgs a, int fmt, cudaStream_t st)
         if (fmt == SQ_MXFP4) return launch_pdl(fp4::k_fp4_dequant<DT, VEC, fp4::FMT_MX, ROWS>, grid, block, 0, st, a);
         return launch_pdl(fp4::k_fp4_dequant<DT, VEC, fp4::FMT_NV, ROWS>, grid, block, 0, st, a);
     };
-    if (few_units(DT, a.rows, a.K)) return by_format(std::integral_constant<int, 1>());
-    return by_format(std::integral_constant<int, 4>());
+    if constexpr (VEC != 0) {
+        if (!few_units(DT, a.rows, a.K)) return by_format(std::integral_constant<int, 4>());
+    }
+    return by_format(std::integral_constant<int, 1>());
 }
 
 template <int DT>
@@ -129,9 +133,7 @@ cudaError_t launch_dequant_vec(const fp4::DequantArgs &a, int fmt, cudaStream_t 
     const int vec = vec_bytes(a.out, a.K * dtype_size(DT));
     if (vec == 32) return launch_dequant<DT, 32>(a, fmt, st);
     if (vec == 16) return launch_dequant<DT, 16>(a, fmt, st);
-    if (vec >= 4) return launch_dequant<DT, 4>(a, fmt, st);
-    if constexpr (DT != DT_F32) return launch_dequant<DT, 2>(a, fmt, st);
-    return cudaErrorInvalidValue;      // fp32 rows are 4-byte aligned
+    return launch_dequant<DT, 0>(a, fmt, st);
 }
 
 // ------------------------------------------------------------------ product
