@@ -127,15 +127,11 @@ __device__ __forceinline__ void load_scale_words(uint32_t *d, uint32_t a)
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "r"(a) : "memory");
 }
 
-// N words (4, 8 or 16) of this thread's TMEM lane from registers.
+// N words (8 or 16) of this thread's TMEM lane from registers.
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t *r)
 {
-    if constexpr (N == 4)
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-                     "r"(r[2]), "r"(r[3])
-                     : "memory");
-    else if constexpr (N == 8)
+    if constexpr (N == 8)
         asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
                      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                      : "memory");
@@ -149,7 +145,8 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t *r)
 template <int N>
 __device__ __forceinline__ void tmem_st_all(uint32_t taddr, const uint32_t *r)
 {
-    constexpr int S = N % 16 == 0 ? 16 : N % 8 == 0 ? 8 : 4;
+    static_assert(N % 8 == 0, "whole stores");
+    constexpr int S = N % 16 == 0 ? 16 : 8;
 #pragma unroll
     for (int i = 0; i < N; i += S) tmem_st<S>(taddr + i, r + i);
 }
@@ -482,27 +479,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 2)
 constexpr int PAIR_THREADS = 352;      // gemm.cuh's six warps, four scale warps, the scale producer
 
 constexpr int SF_BUFS_MX = 4, SF_BUFS_NV = 2;
-constexpr int SF_SLOTS_MIN(int fmt) { return fmt == FMT_MX ? 4 : 4; }
+constexpr int SF_SLOTS_MIN = 4;
 
-template <int BN, int KBO, int FMT>
+template <int BN, int FMT>
 struct Pair4Cfg {
     using Sf = SfT<FMT>;
-    static constexpr int A_KB = BM * BKB, B_KB = (BN / 2) * BKB;
-    static constexpr int A_BYTES = A_KB * KBO, B_BYTES = B_KB * KBO;
+    static constexpr int A_BYTES = BM * BKB, B_BYTES = (BN / 2) * BKB;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int NB = (BN % 128) == 0 ? BN / 128 : BN / 128 + 1;     // row tiles of B's scales
-    static constexpr int SFA_BYTES = KBO * Sf::TILES * SF_TILE, SFB_BYTES = NB * SFA_BYTES;
+    static constexpr int SFA_BYTES = Sf::TILES * SF_TILE, SFB_BYTES = NB * SFA_BYTES;
     static constexpr int SF_BYTES = SFA_BYTES + SFB_BYTES;                   // a scale slot
     static constexpr int STG_TOTAL = 4 * 2 * STG_BYTES;     // two buffers a warp, 32 rows x 128 bytes each
     static constexpr int COLS_BYTES = 2 * 256 * 4;          // the tile's bias, two tiles
     static constexpr int FIXED_BYTES = 1024 + STG_TOTAL + COLS_BYTES + 512;
     static constexpr int ROOM = 227 * 1024 - FIXED_BYTES;
-    static constexpr int STAGES_RAW = (ROOM - SF_SLOTS_MIN(FMT) * SF_BYTES) / STAGE_BYTES;
+    static constexpr int STAGES_RAW = (ROOM - SF_SLOTS_MIN * SF_BYTES) / STAGE_BYTES;
     static constexpr int STAGES = STAGES_RAW > 10 ? 10 : STAGES_RAW;
     static constexpr int SLOTS_RAW = (ROOM - STAGES * STAGE_BYTES) / SF_BYTES;
     static constexpr int SLOTS = SLOTS_RAW > 8 ? 8 : SLOTS_RAW;
     static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * STAGE_BYTES + SLOTS * SF_BYTES;
-    static constexpr int SFA_COLS = KBO * Sf::TILES * 4, SFB_COLS = NB * SFA_COLS;
+    static constexpr int SFA_COLS = Sf::TILES * 4, SFB_COLS = NB * SFA_COLS;
     static constexpr int SF_COLS = SFA_COLS + SFB_COLS;     // of one stage
     static constexpr int SF_BUFS = FMT == FMT_MX ? SF_BUFS_MX : SF_BUFS_NV;
     static constexpr int ACC_ROOM = (512 - SF_BUFS * SF_COLS - BN) / 32 * 32;
@@ -625,13 +621,13 @@ __device__ __forceinline__ void epilogue_pair(const Fp4Params &fp, const CUtenso
     }
 }
 
-template <int BN, int KBO, int FMT>
+template <int BN, int FMT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
     k_fp4_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                const __grid_constant__ CUtensorMap map_as, const __grid_constant__ CUtensorMap map_bs,
                const __grid_constant__ CUtensorMap map_o, const Fp4Params fp)
 {
-    using C = Pair4Cfg<BN, KBO, FMT>;
+    using C = Pair4Cfg<BN, FMT>;
     using Sf = SfT<FMT>;
     constexpr int S = C::STAGES;
     const Params &p = fp.p;
@@ -725,13 +721,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
                     if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), 2 * C::STAGE_BYTES);
                     const uint32_t fb = ptx::map_to_rank(full_bar(stage), 0);
                     const uint32_t sa = sbase + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
-                    if constexpr (KBO == 1) {
-                        ptx::tma_load_2d_pair(sa, &map_a, fb, kb * BKB, ya);
-                        ptx::tma_load_2d_pair(sb, &map_b, fb, kb * BKB, yb);
-                    } else {
-                        ptx::tma_load_3d_pair(sa, &map_a, fb, 0, ya, kb * KBO);
-                        ptx::tma_load_3d_pair(sb, &map_b, fb, 0, yb, kb * KBO);
-                    }
+                    ptx::tma_load_2d_pair(sa, &map_a, fb, kb * BKB, ya);
+                    ptx::tma_load_2d_pair(sb, &map_b, fb, kb * BKB, yb);
                 }
                 __syncwarp();
                 ++issued;
@@ -774,16 +765,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
                     const uint32_t sa = sbase + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
                     const uint32_t sfa0 = tmem_base + C::SF_COL0 + buf * C::SF_COLS, sfb0 = sfa0 + C::SFA_COLS + shift;
                     if (issuer) {
+                        const uint64_t ad = ptx::sdesc_kmajor_sw128(sa), bd = ptx::sdesc_kmajor_sw128(sb);
 #pragma unroll
-                        for (int j = 0; j < KBO; ++j) {
-                            const uint64_t ad = ptx::sdesc_kmajor_sw128(sa + j * C::A_KB);
-                            const uint64_t bd = ptx::sdesc_kmajor_sw128(sb + j * C::B_KB);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int t = j * Sf::TILES + k / Sf::MMAS;
-                                mma_fp4<FMT, 2>(d, ad + 2 * k, bd + 2 * k, idesc_fp4<FMT>(256, BN, (k % Sf::MMAS) * 2),
-                                                sfa0 + 4 * t, sfb0 + 4 * C::NB * t, (kb > 0 || j > 0 || k > 0) ? 1u : 0u);
-                            }
+                        for (int k = 0; k < 4; ++k) {
+                            const int t = k / Sf::MMAS;
+                            mma_fp4<FMT, 2>(d, ad + 2 * k, bd + 2 * k, idesc_fp4<FMT>(256, BN, (k % Sf::MMAS) * 2),
+                                            sfa0 + 4 * t, sfb0 + 4 * C::NB * t, (kb > 0 || k > 0) ? 1u : 0u);
                         }
                         ptx::tc_commit_pair_mc(empty_bar(stage), 0x3);
                     }
@@ -817,8 +804,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
                     const uint32_t fb = sf_full_bar(slot);
                     const uint32_t ssa = sf_base + slot * C::SF_BYTES;
                     ptx::mbar_arrive_expect_tx(fb, C::SF_BYTES);
-                    ptx::tma_load_3d(ssa, &map_as, fb, 0, kb * KBO * Sf::TILES, ta);
-                    ptx::tma_load_3d(ssa + C::SFA_BYTES, &map_bs, fb, 0, kb * KBO * Sf::TILES, tc * BN / 128);
+                    ptx::tma_load_3d(ssa, &map_as, fb, 0, kb * Sf::TILES, ta);
+                    ptx::tma_load_3d(ssa + C::SFA_BYTES, &map_bs, fb, 0, kb * Sf::TILES, tc * BN / 128);
                 }
                 __syncwarp();
                 ++issued;
@@ -849,11 +836,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
                 const uint32_t ssa = sf_base + slot * C::SF_BYTES + lane * 16, ssb = ssa + C::SFA_BYTES;
                 uint32_t r[C::SF_COLS];
 #pragma unroll
-                for (int i = 0; i < KBO * Sf::TILES; ++i) {
+                for (int i = 0; i < Sf::TILES; ++i) {
                     load_scale_words(r + 4 * i, ssa + i * SF_TILE);
 #pragma unroll
                     for (int t = 0; t < C::NB; ++t)
-                        load_scale_words(r + C::SFA_COLS + 4 * (i * C::NB + t), ssb + (t * KBO * Sf::TILES + i) * SF_TILE);
+                        load_scale_words(r + C::SFA_COLS + 4 * (i * C::NB + t), ssb + (t * Sf::TILES + i) * SF_TILE);
                 }
                 if (n >= C::SF_BUFS) {         // the MMAs that read this buffer have completed
                     ok = wait(empty_bar(old), ophase, ERR_MMA + 5);

@@ -296,27 +296,22 @@ inline PairPlan plan_pair(int64_t M, int64_t N, int64_t num_kb)
     return best;
 }
 
-template <int BN, int KBO, int FMT>
+template <int BN, int FMT>
 sq_status launch_fp4_pair(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_t st)
 {
-    using C = fp4::Pair4Cfg<BN, KBO, FMT>;
+    using C = fp4::Pair4Cfg<BN, FMT>;
     gemm::Params &p = fp.p;
     CUtensorMap ma, mb, mas, mbs, mo;
-    if constexpr (KBO == 1) {
-        if (!make_map(&ma, o.xq, false, o.row_bytes, p.M, gemm::BM)) return SQ_ERR_CUDA;
-        if (!make_map(&mb, o.wq, false, o.row_bytes, p.N, BN / 2)) return SQ_ERR_CUDA;
-    } else {
-        if (!make_map3(&ma, o.xq, o.row_bytes, p.M, gemm::BM, KBO)) return SQ_ERR_CUDA;
-        if (!make_map3(&mb, o.wq, o.row_bytes, p.N, BN / 2, KBO)) return SQ_ERR_CUDA;
-    }
-    const uint32_t kt = KBO * fp4::SfT<FMT>::TILES;
+    if (!make_map(&ma, o.xq, false, o.row_bytes, p.M, gemm::BM)) return SQ_ERR_CUDA;
+    if (!make_map(&mb, o.wq, false, o.row_bytes, p.N, BN / 2)) return SQ_ERR_CUDA;
+    const uint32_t kt = fp4::SfT<FMT>::TILES;
     if (!make_scale_map(&mas, o.xs, o.ktiles, p.M, kt, 1)) return SQ_ERR_CUDA;
     if (!make_scale_map(&mbs, o.ws, o.ktiles, p.N, kt, C::NB)) return SQ_ERR_CUDA;
     std::memset(&mo, 0, sizeof(mo));
     // TMA stores need 16-byte row strides and base
     fp.direct = !aligned16(p.out) || (static_cast<int64_t>(p.N) * dtype_size(p.out_dt)) % 16 != 0;
     if (!fp.direct && !make_out_map128(&mo, p.out, p.out_dt, p.M, p.N)) return SQ_ERR_CUDA;
-    p.num_kb = static_cast<int>(cdiv(o.row_bytes, 128 * KBO));
+    p.num_kb = static_cast<int>(cdiv(o.row_bytes, 128));
     const int64_t tr = cdiv(p.M, 2 * gemm::BM), tc = cdiv(p.N, BN);
     if (tr * tc >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
     p.tiles_r = static_cast<int>(tr);
@@ -324,7 +319,7 @@ sq_status launch_fp4_pair(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_t 
     p.num_units = static_cast<int>(tr * tc);
     p.timeout_ns = g_timeout_ns;
     p.inject = g_inject & 1;
-    auto kern = fp4::k_fp4_pair<BN, KBO, FMT>;
+    auto kern = fp4::k_fp4_pair<BN, FMT>;
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), C::SMEM_BYTES);
     if (e != cudaSuccess) return cuda_fail(e);
     int max_clusters = 0;
@@ -359,9 +354,9 @@ sq_status dispatch_fp4(const fp4::Fp4Params &fp, const Fp4Operands &o, cudaStrea
     const PairPlan pair = plan_pair(M, N, kb);
     if (swap.us >= 0 && swap.us < pair.us) return run_fp4_swap<FMT>(fp, o, swap, st);
     switch (pair.bn) {
-    case 256: return launch_fp4_pair<256, 1, FMT>(fp, o, st);
-    case 192: return launch_fp4_pair<192, 1, FMT>(fp, o, st);
-    default: return launch_fp4_pair<128, 1, FMT>(fp, o, st);
+    case 256: return launch_fp4_pair<256, FMT>(fp, o, st);
+    case 192: return launch_fp4_pair<192, FMT>(fp, o, st);
+    default: return launch_fp4_pair<128, FMT>(fp, o, st);
     }
 }
 
