@@ -8,7 +8,8 @@ pass raw pointers and sizes to the library, and raise ``SQError`` on a
 non-OK status.  Every step of the layer runs in the library's kernels; there
 is no CPU path.  Importing this package on a machine without the built
 library raises ``ImportError`` (build it with
-``python w8a8_post_quantization_calib_b200/build.py``).
+``python w8a8_post_quantization_calib_b200/build.py``); so does the first 4-bit
+or key/value call without ``_sqbind``, which the other calls do not need.
 
 Names follow the C ABI: ``calib_absmax``, ``smooth_scales``,
 ``quant_weight``, ``smooth_quant_act``, ``linear_w8a8`` (+ ``gemm_s32``,
@@ -27,6 +28,7 @@ key/value cache ``kv_cache_write``, ``kv_cache_read``.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 
 import torch
@@ -133,11 +135,25 @@ def _load() -> ctypes.CDLL:
 
 _lib = _load()
 
-if not os.path.exists(os.path.join(_HERE, "_sqbind.so")):
-    raise ImportError(f"{_HERE}/_sqbind.so is missing: build it with `python w8a8_post_quantization_calib_b200/build.py`")
-from . import _sqbind  # noqa: E402  (links libsq.so, loaded above)
 
-_sqbind.set_error(SQError)
+class _Binding:
+    """The native module _sqbind, loaded (and put in this object's place) by the first call that needs it."""
+
+    def __getattr__(self, name):
+        global _bind
+        hint = "build it with `python w8a8_post_quantization_calib_b200/build.py`"
+        try:
+            module = importlib.import_module(__name__ + "._sqbind")            # links libsq.so, loaded above
+        except ImportError as e:
+            raise ImportError(f"{_HERE}/_sqbind.so is missing or does not fit this Python and torch ({e}): {hint}") from e
+        if module.TORCH_VERSION != torch.__version__.split("+")[0]:
+            raise ImportError(f"{_HERE}/_sqbind.so was built for torch {module.TORCH_VERSION}, not {torch.__version__}: {hint}")
+        module.set_error(SQError)
+        _bind = module
+        return getattr(module, name)
+
+
+_bind = _Binding()
 
 
 def lib() -> ctypes.CDLL:
@@ -470,7 +486,7 @@ def fp4_scale_bytes(fmt: int, rows: int, K: int) -> int:
 
 def smooth_scales_nvfp4(act_max, w_max, alpha: float, s, g_act=None, g_w=None, stream=None) -> None:
     """smooth_scales with NVFP4's tensor scales of the smoothed activations and weight (fp32 [1] each, or None)."""
-    _sqbind.smooth_scales_nvfp4(act_max, w_max, alpha, s, g_act, g_w, stream)
+    _bind.smooth_scales_nvfp4(act_max, w_max, alpha, s, g_act, g_w, stream)
 
 
 def quant_weight_fp4(w, s, fmt: int, wq4, w_sf, g=None, stream=None) -> None:
@@ -478,22 +494,22 @@ def quant_weight_fp4(w, s, fmt: int, wq4, w_sf, g=None, stream=None) -> None:
 
     s: fp32 [K] or None; g: NVFP4's tensor scale, fp32 [1] or None (1).
     """
-    _sqbind.quant_weight_fp4(w, s, fmt, wq4, w_sf, g, stream)
+    _bind.quant_weight_fp4(w, s, fmt, wq4, w_sf, g, stream)
 
 
 def smooth_quant_act_fp4(x, s, fmt: int, xq4, x_sf, g=None, stream=None) -> None:
     """4-bit blocks of x * recip(s_j) for a 2-D x whose rows may lie in wider ones; arguments as quant_weight_fp4."""
-    _sqbind.smooth_quant_act_fp4(x, s, fmt, xq4, x_sf, g, stream)
+    _bind.smooth_quant_act_fp4(x, s, fmt, xq4, x_sf, g, stream)
 
 
 def dequant_fp4(q4, sf, fmt: int, out, g=None, stream=None) -> None:
     """out [rows, K] = the values that the codes stand for, rounded to out's type."""
-    _sqbind.dequant_fp4(q4, sf, fmt, out, g, stream)
+    _bind.dequant_fp4(q4, sf, fmt, out, g, stream)
 
 
 def linear_fp4(xq4, x_sf, wq4, w_sf, fmt: int, y, bias=None, g_act=None, g_w=None, stream=None) -> None:
     """y [M, N] = packed activations times packed weight of one format (K: the codes' row length), plus bias."""
-    _sqbind.linear_fp4(xq4, x_sf, wq4, w_sf, fmt, y, bias, g_act, g_w, stream)
+    _bind.linear_fp4(xq4, x_sf, wq4, w_sf, fmt, y, bias, g_act, g_w, stream)
 
 
 # ---------------------------------------------------------------- quantised key/value cache
@@ -520,7 +536,7 @@ def kv_cache_write(k, v, slots, fmt: int, k_cache, k_scale, v_cache, v_scale, st
     KV_INT8, else uint8) [pages, page_size, H, kv_row_bytes], scales float32 [pages, page_size, H], or uint8
     [pages, page_size, H, ceil(D / 32)] for KV_MXFP4.  A slot behind the cache is not written; sync_status reports it.
     """
-    _sqbind.kv_cache_write(k, v, slots, fmt, k_cache, k_scale, v_cache, v_scale, stream)
+    _bind.kv_cache_write(k, v, slots, fmt, k_cache, k_scale, v_cache, v_scale, stream)
 
 
 def kv_cache_read(fmt: int, k_cache, k_scale, v_cache, v_scale, table, cu_rows, k_out, v_out, starts=None,
@@ -530,4 +546,4 @@ def kv_cache_read(fmt: int, k_cache, k_scale, v_cache, v_scale, table, cu_rows, 
     table: int32 [B, max_pages]; cu_rows: int32 [B + 1], sequence b's output rows are cu_rows[b] .. cu_rows[b + 1] - 1
     and hold its positions from starts[b] (int32 [B]; None: 0) on.  Rows outside are left as they were.
     """
-    _sqbind.kv_cache_read(fmt, k_cache, k_scale, v_cache, v_scale, table, cu_rows, k_out, v_out, starts, stream)
+    _bind.kv_cache_read(fmt, k_cache, k_scale, v_cache, v_scale, table, cu_rows, k_out, v_out, starts, stream)

@@ -4,6 +4,7 @@ sm_100a, and _sqbind.so (libsq's calls for PyTorch tensors) with the host
 compiler against the installed torch."""
 from __future__ import annotations
 
+import importlib.metadata
 import importlib.util
 import os
 import subprocess
@@ -25,6 +26,7 @@ PEAK_SOURCES = ["peak.cu"]
 PEAK_HEADERS = ["common.cuh", "ptx_sm100.cuh"]
 BIND_SO = os.path.join(HERE, "_sqbind.so")
 BIND_SOURCES = ["bind.cpp"]
+BIND_STAMP = os.path.join(OBJ, "_sqbind.versions")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
@@ -63,6 +65,18 @@ def _bind_cmd(out: str) -> list[str]:
             "-ltorch_cpu", "-ltorch_python", "-L" + HERE, "-l:libsq.so", "-Wl,-rpath,$ORIGIN"]
 
 
+def _bind_versions() -> str:
+    """What _sqbind.so is compiled against besides its sources: another Python or torch makes it stale."""
+    return f"python {sys.version} {sysconfig.get_config_var('SOABI')}\ntorch {importlib.metadata.version('torch')}\n"
+
+
+def _bind_stale(so: str, stamp: str) -> bool:
+    if _stale(so, BIND_SOURCES, []) or not os.path.exists(stamp):
+        return True
+    with open(stamp) as f:
+        return f.read() != _bind_versions()
+
+
 def _run(jobs, verbose: bool) -> None:
     """Runs compilers side by side.  A job is (temporary, final, command): what a command has made takes its final
     name; the first failure is raised after all have ended."""
@@ -99,8 +113,10 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     objs = [os.path.join(OBJ, unit[:-3] + ".o") for unit in UNITS]
     if force or not os.path.exists(SO) or any(os.path.getmtime(o) > os.path.getmtime(SO) for o in objs):
         _run([job(SO, ["-shared", *objs], None)], verbose)
-    if force or _stale(BIND_SO, BIND_SOURCES, []):
+    if force or _bind_stale(BIND_SO, BIND_STAMP):
         _run([(BIND_SO + tag, BIND_SO, _bind_cmd(BIND_SO + tag))], verbose)
+        with open(BIND_STAMP, "w") as f:
+            f.write(_bind_versions())
     return SO
 
 

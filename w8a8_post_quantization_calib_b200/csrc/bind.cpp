@@ -15,6 +15,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/headeronly/version.h>
 
 #include <string>
 
@@ -113,6 +114,7 @@ public:
         const sq_status st = f(args...);
         PyEval_RestoreThread(state);
         if (st == SQ_OK) Py_RETURN_NONE;
+        if (g_error == nullptr) raise(PyExc_RuntimeError, std::string(name_) + " returned status " + std::to_string(st));
         PyObject *e = PyObject_CallFunction(g_error, "si", name_, static_cast<int>(st));
         if (e != nullptr) {
             PyErr_SetObject(g_error, e);
@@ -375,4 +377,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_sqbind", nullptr, -1, methods, nu
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__sqbind() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__sqbind()
+{
+    PyObject *m = PyModule_Create(&module);
+    if (m != nullptr && PyModule_AddStringConstant(m, "TORCH_VERSION", TORCH_VERSION) != 0) Py_CLEAR(m);
+    return m;
+}
