@@ -85,3 +85,27 @@ def test_another_python_or_torch_makes_the_binding_stale(tmp_path, monkeypatch):
     assert not b._bind_stale(str(so), str(stamp))
     os.utime(so, (0, 0))                                             # sources newer than the module
     assert b._bind_stale(str(so), str(stamp))
+
+
+def test_tensors_of_the_wrong_kind_raise_what_the_other_calls_raise():
+    """A tensor on the CPU is a TypeError, as in the INT8 and FP8 calls, and a ValueError."""
+    torch = pytest.importorskip("torch")
+    sq = pytest.importorskip(PKG)
+    x, q, s = torch.zeros(4, 64), torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(64)
+    kv, slots, i32 = torch.zeros(4, 2, 32), torch.arange(4), torch.zeros(1, 1, dtype=torch.int32)
+    calls = [
+        lambda: sq.smooth_quant_act(x, s, sq.ACT_STATIC, s, q),
+        lambda: sq.smooth_quant_act_fp4(x, s, sq.MXFP4, q, q),
+        lambda: sq.quant_weight_fp4(x, s, sq.MXFP4, q, q),
+        lambda: sq.dequant_fp4(q, q, sq.MXFP4, x),
+        lambda: sq.linear_fp4(q, q, q, q, sq.MXFP4, x),
+        lambda: sq.smooth_scales_nvfp4(s, s, 0.5, s),
+        lambda: sq.kv_cache_write(kv, kv, slots, sq.KV_INT8, q, s, q, s),
+        lambda: sq.kv_cache_read(sq.KV_INT8, q, s, q, s, i32, i32[0], kv, kv),
+    ]
+    for n, call in enumerate(calls):
+        with pytest.raises(TypeError, match="CUDA tensor"):
+            call()
+        if n:
+            with pytest.raises(ValueError, match="CUDA tensor"):
+                call()

@@ -6,8 +6,11 @@
 //
 // Positional arguments only; the Python functions of the package give them
 // names and defaults.  Every function returns None or raises: TypeError (not a
-// tensor, wrong type), ValueError (shape, device, contiguity), and, through
-// the package's SQError, any status that the C ABI returns.
+// CUDA tensor, wrong type), ValueError (shape, device, contiguity), and, through
+// the package's SQError, any status that the C ABI returns.  A tensor that is
+// not on a GPU, and an operand of the wrong type beside another one, raise an
+// error that is both: the package's other calls raise TypeError there, these
+// raised ValueError before.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -24,6 +27,7 @@
 namespace {
 
 PyObject *g_error = nullptr;       // SQError(function, status)
+PyObject *g_kind_error = nullptr;  // TypeError and ValueError
 
 struct Raised {};                  // a Python exception is set
 
@@ -55,10 +59,19 @@ public:
     {
         if (!THPVariable_Check(args_[i])) raise(PyExc_TypeError, std::string(what) + " must be a CUDA tensor");
         const at::Tensor &t = THPVariable_Unpack(args_[i]);
-        if (!t.is_cuda()) raise(PyExc_ValueError, std::string(what) + " must be a CUDA tensor, got one on " + t.device().str());
+        if (!t.is_cuda()) raise(g_kind_error, std::string(what) + " must be a CUDA tensor, got one on " + t.device().str());
         if (t.device().index() != device())
             raise(PyExc_ValueError, std::string("every tensor must be on the current device cuda:") + std::to_string(device()) + ", got " +
                                         what + " on " + t.device().str());
+        return t;
+    }
+
+    // tensor of a type
+    const at::Tensor &typed(int i, const char *what, at::ScalarType type) const
+    {
+        const at::Tensor &t = tensor(i, what);
+        if (t.scalar_type() != type)
+            raise(g_kind_error, std::string(what) + " must be " + c10::toString(type) + ", got " + c10::toString(t.scalar_type()));
         return t;
     }
 
@@ -242,8 +255,8 @@ PyObject *linear_fp4(const Call &c)
     const Operand x = operand(c, 0, M, K, fmt, "activation codes"), w = operand(c, 2, N, K, fmt, "weight codes");
     const void *bias = nullptr;
     if (!c.none(6)) {
-        const at::Tensor &b = c.tensor(6, "bias");
-        if (b.scalar_type() != y.scalar_type() || b.numel() != N || !b.is_contiguous())
+        const at::Tensor &b = c.typed(6, "bias", y.scalar_type());
+        if (b.numel() != N || !b.is_contiguous())
             raise(PyExc_ValueError, std::string("bias must be a contiguous ") + c10::toString(y.scalar_type()) + " tensor of " + std::to_string(N) + " elements");
         bias = b.data_ptr();
     }
@@ -265,15 +278,15 @@ Cache cache(const Call &c, int i, sq_kv_format fmt, int64_t H, int64_t D)
     Cache r{};
     for (int n = 0; n < 4; ++n) {
         const bool scale = n & 1;
-        const at::Tensor &t = c.tensor(i + n, names[n]);
+        const at::ScalarType type = scale ? (fmt == SQ_KV_MXFP4 ? at::kByte : at::kFloat) : fmt == SQ_KV_INT8 ? at::kChar : at::kByte;
+        const at::Tensor &t = c.typed(i + n, names[n], type);
         if (n == 0) {
             if (t.dim() != 4) raise(PyExc_ValueError, "k_cache must be 4-D, got " + shape_of(t));
             r.pages = t.size(0);
             r.page_size = t.size(1);
         }
-        const at::ScalarType type = scale ? (fmt == SQ_KV_MXFP4 ? at::kByte : at::kFloat) : fmt == SQ_KV_INT8 ? at::kChar : at::kByte;
         const int64_t last = !scale ? rb : fmt == SQ_KV_MXFP4 ? sb : 0;           // 0: no such dimension
-        if (t.scalar_type() != type || !t.is_contiguous() || t.dim() != (last ? 4 : 3) || t.size(0) != r.pages ||
+        if (!t.is_contiguous() || t.dim() != (last ? 4 : 3) || t.size(0) != r.pages ||
             t.size(1) != r.page_size || t.size(2) != H || (last && t.size(3) != last))
             raise(PyExc_ValueError, std::string(names[n]) + " must be a contiguous " + c10::toString(type) + " tensor [" + std::to_string(r.pages) +
                                         ", " + std::to_string(r.page_size) + ", " + std::to_string(H) + (last ? ", " + std::to_string(last) : "") +
@@ -300,8 +313,8 @@ PyObject *kv_cache_write(const Call &c)
         if (T > 1 && x.stride(0) < H * D) raise(PyExc_ValueError, std::string("the tokens of ") + what + " must not overlap");
         ld[n] = T > 1 ? x.stride(0) : H * D;
     }
-    const at::Tensor &slots = c.tensor(2, "slots");
-    if (slots.scalar_type() != at::kLong || slots.dim() != 1 || slots.size(0) != T || !slots.is_contiguous())
+    const at::Tensor &slots = c.typed(2, "slots", at::kLong);
+    if (slots.dim() != 1 || slots.size(0) != T || !slots.is_contiguous())
         raise(PyExc_ValueError, "slots must be a contiguous int64 tensor [" + std::to_string(T) + "]");
     const sq_kv_format fmt = kv_format(c.integer(3));
     const Cache a = cache(c, 4, fmt, H, D);
@@ -320,16 +333,16 @@ PyObject *kv_cache_read(const Call &c)
     const sq_dtype dt = dtype_of(ko);
     const sq_kv_format fmt = kv_format(c.integer(0));
     const Cache a = cache(c, 1, fmt, H, D);
-    const at::Tensor &table = matrix(c.tensor(5, "table"), "table");
+    const at::Tensor &table = matrix(c.typed(5, "table", at::kInt), "table");
     const int64_t B = table.size(0), pages = table.size(1);
     auto ints = [](const at::Tensor &t, int64_t dim, int64_t n, const char *what) {
-        if (t.scalar_type() != at::kInt || !t.is_contiguous() || t.dim() != dim || t.numel() != n)
+        if (!t.is_contiguous() || t.dim() != dim || t.numel() != n)
             raise(PyExc_ValueError, std::string(what) + " must be a contiguous int32 tensor of " + std::to_string(n) + " elements, got " +
                                         c10::toString(t.scalar_type()) + " " + shape_of(t));
         return static_cast<const int32_t *>(t.data_ptr());
     };
-    const int32_t *tab = ints(table, 2, B * pages, "table"), *cu = ints(c.tensor(6, "cu_rows"), 1, B + 1, "cu_rows");
-    const int32_t *starts = c.none(9) ? nullptr : ints(c.tensor(9, "starts"), 1, B, "starts");
+    const int32_t *tab = ints(table, 2, B * pages, "table"), *cu = ints(c.typed(6, "cu_rows", at::kInt), 1, B + 1, "cu_rows");
+    const int32_t *starts = c.none(9) ? nullptr : ints(c.typed(9, "starts", at::kInt), 1, B, "starts");
     return c.call(sq_kv_cache_read, fmt, a.p[0], a.p[1], a.p[2], a.p[3], a.pages, a.page_size, H, D, tab, B, pages, cu, starts, total, dt,
                                    ko.data_ptr(), vo.data_ptr(), c.stream(10));
 }
@@ -379,7 +392,16 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_sqbind", nullptr, -1, methods, nu
 
 PyMODINIT_FUNC PyInit__sqbind()
 {
+    if (g_kind_error == nullptr) {
+        PyObject *bases = PyTuple_Pack(2, PyExc_TypeError, PyExc_ValueError);
+        if (bases == nullptr) return nullptr;
+        g_kind_error = PyErr_NewException("w8a8_post_quantization_calib_b200._sqbind.TensorKindError", bases, nullptr);
+        Py_DECREF(bases);
+        if (g_kind_error == nullptr) return nullptr;
+    }
     PyObject *m = PyModule_Create(&module);
-    if (m != nullptr && PyModule_AddStringConstant(m, "TORCH_VERSION", TORCH_VERSION) != 0) Py_CLEAR(m);
+    if (m != nullptr && (PyModule_AddStringConstant(m, "TORCH_VERSION", TORCH_VERSION) != 0 ||
+                         PyModule_AddObjectRef(m, "TensorKindError", g_kind_error) != 0))
+        Py_CLEAR(m);
     return m;
 }
