@@ -573,7 +573,7 @@ sq_status sq_linear_fp4(const uint8_t *xq4, const uint8_t *x_sf, const uint8_t *
  * position in the page.  k_cache, v_cache: [slots, H, sq_kv_row_bytes(fmt, D)]
  * bytes (the codes behind D are 0); k_scale, v_scale: [slots, H,
  * sq_kv_scale_bytes(fmt, D)] bytes (one fp32, or ceil(D / 32) E8M0 bytes).
- * All four 16-byte aligned.  1 <= D <= 1024, else SQ_ERR_UNSUPPORTED.
+ * All four 16-byte aligned.  D <= 1024 and H <= 65536, else SQ_ERR_UNSUPPORTED.
  *
  * Indices are checked on the device: a slot or page outside the cache is not
  * accessed, and sq_sync_status then returns SQ_ERR_INVALID_ARG (once).

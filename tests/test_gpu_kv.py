@@ -331,3 +331,29 @@ def test_python_checks():
         sq.kv_cache_read(fmt, *c[:2], c[2][:1], c[3], table, cu, k, k.clone())
     with pytest.raises(ValueError):
         sq.kv_row_bytes(fmt, 1025)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_no_pages(fmt):
+    """A cache without pages and a table without columns: every index is outside, padding is skipped, rows are zeros."""
+    T, H, D = 3, 8, 128
+    x = dev(rand_x(3, (T, H, D), F16), F16)
+    none = _cache(0, 4, H, D, fmt)
+    sq.kv_cache_write(x, x, dev(np.array([-1, -7, -1])), fmt, *none)
+    _sync()
+    sq.kv_cache_write(x, x, dev(np.array([-1, 0, -1])), fmt, *none)
+    assert sq.sync_status() == 1
+    some = _cache(2, 4, H, D, fmt)
+    sq.kv_cache_write(x, x, dev(np.arange(T)), fmt, *some)
+    _sync()
+    cu = dev(np.array([1, 1, 3], np.int32))
+    for cache, table in ((none, np.zeros((2, 2), np.int32)), (some, np.zeros((2, 0), np.int32)), (none, np.zeros((2, 0), np.int32))):
+        ko, vo = (torch.full((5, H, D), 7.0, dtype=torch.float16, device="cuda") for _ in "kv")
+        sq.kv_cache_read(fmt, *cache, dev(table), cu, ko, vo)
+        assert sq.sync_status() == 1
+        for o in (ko, vo):
+            assert torch.all(o[1:3] == 0) and torch.all(o[:1] == 7.0) and torch.all(o[3:] == 7.0)
+        ko.fill_(7.0)
+        sq.kv_cache_read(fmt, *cache, dev(table), cu * 0, ko, vo)          # no rows at all
+        _sync()
+        assert torch.all(ko == 7.0)

@@ -501,10 +501,11 @@ sq_status sq_kv_cache_write(const void *k, const void *v, sq_dtype dt, int64_t T
     if (r != SQ_OK) return r;
     if (T < 0 || k_ld < H * D || v_ld < H * D || num_slots < 0) return SQ_ERR_INVALID_ARG;
     if (T == 0) return SQ_OK;
-    if (k == nullptr || v == nullptr || slots == nullptr || k_cache == nullptr || k_scale == nullptr ||
-        v_cache == nullptr || v_scale == nullptr)
+    if (k == nullptr || v == nullptr || slots == nullptr) return SQ_ERR_INVALID_ARG;
+    // a cache without slots has no address, and none of it is accessed
+    if (num_slots > 0 && (k_cache == nullptr || k_scale == nullptr || v_cache == nullptr || v_scale == nullptr))
         return SQ_ERR_INVALID_ARG;
-    if (num_slots > (int64_t(1) << 40) || k_ld > (int64_t(1) << 32) || v_ld > (int64_t(1) << 32))
+    if (T > (int64_t(1) << 31) || num_slots > (int64_t(1) << 40) || k_ld > (int64_t(1) << 32) || v_ld > (int64_t(1) << 32))
         return SQ_ERR_UNSUPPORTED;
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale))
         return SQ_ERR_MISALIGNED;
@@ -517,7 +518,7 @@ sq_status sq_kv_cache_write(const void *k, const void *v, sq_dtype dt, int64_t T
                     static_cast<uint8_t *>(v_cache), k_scale, v_scale, static_cast<int>(H), static_cast<int>(D), ll, 0,
                     inverse63(H)};
     const int64_t steps = cdiv(T * H, 32 >> ll);                // of a warp, for keys and again for values
-    if (T > (int64_t(1) << 31) || cdiv(2 * steps, kv::WARPS) >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
+    if (cdiv(2 * steps, kv::WARPS) >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
     const int es = dtype_size(dt);
     a.vec = std::min(vec_bytes(k, (k_ld * es) | (D * es)), vec_bytes(v, (v_ld * es) | (D * es)));
     const cudaStream_t st = as_stream(stream);
@@ -544,9 +545,11 @@ sq_status sq_kv_cache_read(sq_kv_format fmt, const void *k_cache, const void *k_
     if (r != SQ_OK) return r;
     if (num_pages < 0 || page_size <= 0 || B < 0 || max_pages < 0 || total < 0) return SQ_ERR_INVALID_ARG;
     if (total == 0 || B == 0) return SQ_OK;
-    if (k_cache == nullptr || k_scale == nullptr || v_cache == nullptr || v_scale == nullptr || table == nullptr ||
-        cu_rows == nullptr || k_out == nullptr || v_out == nullptr)
+    if (cu_rows == nullptr || k_out == nullptr || v_out == nullptr) return SQ_ERR_INVALID_ARG;
+    // a cache without pages, a table without columns: no address, no access
+    if (num_pages > 0 && (k_cache == nullptr || k_scale == nullptr || v_cache == nullptr || v_scale == nullptr))
         return SQ_ERR_INVALID_ARG;
+    if (max_pages > 0 && table == nullptr) return SQ_ERR_INVALID_ARG;
     if (num_pages >= (int64_t(1) << 31) || page_size >= (int64_t(1) << 31) || B >= (int64_t(1) << 30) ||
         max_pages >= (int64_t(1) << 31) || total >= (int64_t(1) << 31))
         return SQ_ERR_UNSUPPORTED;
