@@ -99,6 +99,21 @@ void sq_set_wait_timeout_ns(unsigned long long ns);
  * what = 0 turns them off. */
 void sq_debug_inject(int what);
 
+/* Which kernels calls of these sizes run on the current device, by the same
+ * rules and without a launch, so that tests can name what they reach.  `plan`
+ * is host memory.
+ *   sq_debug_linear_fp4_plan  plan[3]: 1 CTA pairs / 0 weights as the A operand; columns (pairs) or
+ *                             tokens of a tile; CTAs of a cluster
+ *   sq_debug_rows_fp4_plan    plan[2]: rows a thread; units of rows that a block walks.  values: 0
+ *                             quantisers, 1 sq_dequant_fp4; vec: bytes (32, 16, 0) that the rows'
+ *                             addresses allow an access
+ *   sq_debug_kv_plan          plan[4]: writes' steps a warp and chunks a lane; reads' kernel (1 rows end
+ *                             to end, 0 warps by token) and warps a token
+ */
+sq_status sq_debug_linear_fp4_plan(int64_t M, int64_t N, int64_t K, int *plan);
+sq_status sq_debug_rows_fp4_plan(int values, int fmt, sq_dtype dt, int vec, int64_t rows, int64_t K, int *plan);
+sq_status sq_debug_kv_plan(int64_t rows, int64_t H, int64_t D, int *plan);
+
 /* Synchronises `stream`, then returns SQ_ERR_TIMEOUT if any kernel of this
  * library recorded a barrier timeout on the current device since the last
  * check, SQ_ERR_INVALID_ARG if a kernel of the key/value cache met an index

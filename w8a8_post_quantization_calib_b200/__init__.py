@@ -59,6 +59,7 @@ EXPORTS = (
     "sq_fp4_code_bytes", "sq_fp4_scale_bytes", "sq_smooth_scales_nvfp4", "sq_quant_weight_fp4",
     "sq_smooth_quant_act_fp4", "sq_dequant_fp4", "sq_linear_fp4",
     "sq_kv_row_bytes", "sq_kv_scale_bytes", "sq_kv_cache_write", "sq_kv_cache_read",
+    "sq_debug_linear_fp4_plan", "sq_debug_rows_fp4_plan", "sq_debug_kv_plan",
 )
 
 
@@ -121,6 +122,9 @@ def _load() -> ctypes.CDLL:
         "sq_smooth_quant_act_fp4": (I, [P, I, I64, I64, I64, P, I, P, P, P, P]),
         "sq_dequant_fp4": (I, [P, P, I, I64, I64, P, I, P, P]),
         "sq_linear_fp4": (I, [P, P, P, P, I, I64, I64, I64, P, P, P, I, P, P]),
+        "sq_debug_linear_fp4_plan": (I, [I64, I64, I64, P]),
+        "sq_debug_rows_fp4_plan": (I, [I, I, I, I, I64, I64, P]),
+        "sq_debug_kv_plan": (I, [I64, I64, I64, P]),
         "sq_kv_row_bytes": (SZ, [I, I64]),
         "sq_kv_scale_bytes": (SZ, [I, I64]),
         "sq_kv_cache_write": (I, [P, P, I, I64, I64, I64, I64, I64, P, I, I64, P, P, P, P, P]),

@@ -62,20 +62,34 @@ inline bool few_units(int dt, int64_t rows, int64_t cols)
     return dt == DT_F32 ? blocks < 4 * sm_count() : 3 * blocks < 2 * sm_count();
 }
 
+// Rows a thread, units of rows and grid of a quantiser or dequantiser whose
+// rows allow accesses of `vec` bytes.
+struct RowsPlan {
+    int rows;
+    int64_t units;
+    dim3 grid;
+};
+
+inline RowsPlan plan_rows(int dt, int vec, int64_t rows, int64_t cols, int per_sm)
+{
+    const bool four = vec >= 16 && !few_units(dt, rows, cols);
+    const int64_t units = four ? fp4::quant_units<4>(rows) : fp4::quant_units<1>(rows);
+    return {four ? 4 : 1, units, strip_grid(units, cols, per_sm)};
+}
+
+// columns a quantiser covers: every byte of the scale tiles
+inline int64_t quant_cols(int fmt, int64_t K) { return fp4::scale_tiles_k(fmt, K) * (fmt == SQ_MXFP4 ? 128 : 64); }
+
 template <int DT, int VEC, int FMT>
 cudaError_t launch_quant(fp4::QuantArgs a, cudaStream_t st)
 {
-    const int64_t cols = fp4::scale_tiles_k(FMT, a.K) * fp4::FmtT<FMT>::TILE_K;    // every byte of the scale tiles
+    const RowsPlan plan = plan_rows(DT, VEC, a.rows, quant_cols(FMT, a.K), QUANT_PER_SM);
     const dim3 block(fp4::QTX, fp4::QTY);
-    auto by_rows = [&](auto rows) {
-        constexpr int ROWS = decltype(rows)::value;
-        a.units = fp4::quant_units<ROWS>(a.rows);
-        return launch_pdl(fp4::k_fp4_quant<DT, VEC, FMT, ROWS>, strip_grid(a.units, cols, QUANT_PER_SM), block, 0, st, a);
-    };
+    a.units = plan.units;
     if constexpr (VEC != 0) {
-        if (!few_units(DT, a.rows, cols)) return by_rows(std::integral_constant<int, 4>());
+        if (plan.rows == 4) return launch_pdl(fp4::k_fp4_quant<DT, VEC, FMT, 4>, plan.grid, block, 0, st, a);
     }
-    return by_rows(std::integral_constant<int, 1>());
+    return launch_pdl(fp4::k_fp4_quant<DT, VEC, FMT, 1>, plan.grid, block, 0, st, a);
 }
 
 template <int DT, int VEC>
@@ -113,16 +127,16 @@ sq_status quant_fp4(const void *x, int dt, int64_t rows, int64_t K, int64_t ld, 
 template <int DT, int VEC>
 cudaError_t launch_dequant(fp4::DequantArgs a, int fmt, cudaStream_t st)
 {
+    const RowsPlan plan = plan_rows(DT, VEC, a.rows, a.K, DEQUANT_PER_SM);
     const dim3 block(fp4::QTX, fp4::QTY);
+    a.units = plan.units;
     auto by_format = [&](auto rows) {
         constexpr int ROWS = decltype(rows)::value;
-        a.units = fp4::quant_units<ROWS>(a.rows);
-        const dim3 grid = strip_grid(a.units, a.K, DEQUANT_PER_SM);
-        if (fmt == SQ_MXFP4) return launch_pdl(fp4::k_fp4_dequant<DT, VEC, fp4::FMT_MX, ROWS>, grid, block, 0, st, a);
-        return launch_pdl(fp4::k_fp4_dequant<DT, VEC, fp4::FMT_NV, ROWS>, grid, block, 0, st, a);
+        if (fmt == SQ_MXFP4) return launch_pdl(fp4::k_fp4_dequant<DT, VEC, fp4::FMT_MX, ROWS>, plan.grid, block, 0, st, a);
+        return launch_pdl(fp4::k_fp4_dequant<DT, VEC, fp4::FMT_NV, ROWS>, plan.grid, block, 0, st, a);
     };
     if constexpr (VEC != 0) {
-        if (!few_units(DT, a.rows, a.K)) return by_format(std::integral_constant<int, 4>());
+        if (plan.rows == 4) return by_format(std::integral_constant<int, 4>());
     }
     return by_format(std::integral_constant<int, 1>());
 }
@@ -345,15 +359,28 @@ sq_status launch_fp4_pair(fp4::Fp4Params fp, const Fp4Operands &o, cudaStream_t 
     return e == cudaSuccess ? check_launch() : cuda_fail(e);
 }
 
+// CTA pairs with tiles of bn columns, or the weights-as-A kernel (cs CTAs a cluster).
+struct LinearPlan {
+    bool pairs;
+    int bn;
+    SwapPlan swap;
+};
+
+inline LinearPlan plan_linear(int64_t M, int64_t N, int64_t num_kb)
+{
+    const SwapPlan swap = plan_swap(M, N, num_kb);
+    if (M <= 128) return {false, swap.bn, swap};
+    const PairPlan pair = plan_pair(M, N, num_kb);
+    if (swap.us >= 0 && swap.us < pair.us) return {false, swap.bn, swap};
+    return {true, pair.bn, swap};
+}
+
 template <int FMT>
 sq_status dispatch_fp4(const fp4::Fp4Params &fp, const Fp4Operands &o, cudaStream_t st)
 {
-    const int64_t M = fp.p.M, N = fp.p.N, kb = cdiv(o.row_bytes, 128);
-    const SwapPlan swap = plan_swap(M, N, kb);
-    if (M <= 128) return run_fp4_swap<FMT>(fp, o, swap, st);
-    const PairPlan pair = plan_pair(M, N, kb);
-    if (swap.us >= 0 && swap.us < pair.us) return run_fp4_swap<FMT>(fp, o, swap, st);
-    switch (pair.bn) {
+    const LinearPlan plan = plan_linear(fp.p.M, fp.p.N, cdiv(o.row_bytes, 128));
+    if (!plan.pairs) return run_fp4_swap<FMT>(fp, o, plan.swap, st);
+    switch (plan.bn) {
     case 256: return launch_fp4_pair<256, FMT>(fp, o, st);
     case 192: return launch_fp4_pair<192, FMT>(fp, o, st);
     default: return launch_fp4_pair<128, FMT>(fp, o, st);
@@ -371,7 +398,40 @@ inline int lanes_log2(int D)
     return l;
 }
 
+constexpr int KV_READ_WARPS = 16;               // warps an SM below which a token's heads are split over warps
 
+// Steps a warp and chunks of 16 elements a lane of a write: several steps once
+// that leaves every SM its 64 warps.
+struct WritePlan {
+    int steps, chunks;
+};
+
+inline WritePlan plan_write(int64_t T, int64_t H, int64_t D)
+{
+    if (D > 512) return {1, 2};
+    const int64_t steps = cdiv(T * H, 32 >> lanes_log2(static_cast<int>(D)));      // of a warp, for keys and again for values
+    return {2 * steps >= static_cast<int64_t>(kv::TOKENS) * 64 * sm_count() ? kv::TOKENS : 1, 1};
+}
+
+// Rows end to end where a warp a token would leave lanes idle or have one
+// group of heads in flight: 1 head of 64 414 -> 60 us (45 at the copy rate), 2
+// of 128 107 -> 58, 5 of 128 59 -> 48; 8 of 128 stay a warp a token (69 us
+// against 73 for 75 k tokens, 2.7 against 3.4 for 64).  Else 2^part_log2 warps
+// a token: more than one while the heads allow and the SMs are not full.
+struct ReadPlan {
+    bool by_rows;
+    int part_log2;
+};
+
+inline ReadPlan plan_read(int64_t total, int64_t H, int64_t D)
+{
+    const int ll = lanes_log2(static_cast<int>(D));
+    const int64_t groups = cdiv(H, 32 >> ll);
+    if (D <= 512 && ((16 << ll) != D || H % (32 >> ll) != 0 || groups < 2)) return {true, 0};
+    int part = 0;
+    while ((int64_t(2) << part) <= groups && (total << part) < static_cast<int64_t>(KV_READ_WARPS) * sm_count()) ++part;
+    return {false, part};
+}
 
 // Calls launch(type, format, access width) with all three as compile-time
 // constants (width 0: narrower than 16 bytes).
@@ -391,8 +451,6 @@ template <typename F> cudaError_t kv_dispatch(int dt, int fmt, int vec, F &&laun
     if (dt == SQ_F16) return format(std::integral_constant<int, DT_F16>());
     return format(std::integral_constant<int, DT_BF16>());
 }
-
-constexpr int KV_READ_WARPS = 16;
 
 // ceil(2^63 / d): the high word of (2 n) * inverse63(d) is n / d as long as n * d < 2^63
 inline uint64_t inverse63(int64_t d) { return ((uint64_t(1) << 63) + static_cast<uint64_t>(d) - 1) / static_cast<uint64_t>(d); }
@@ -483,6 +541,39 @@ sq_status sq_linear_fp4(const uint8_t *xq4, const uint8_t *x_sf, const uint8_t *
     return fmt == SQ_MXFP4 ? dispatch_fp4<fp4::FMT_MX>(fp, o, st) : dispatch_fp4<fp4::FMT_NV>(fp, o, st);
 }
 
+sq_status sq_debug_linear_fp4_plan(int64_t M, int64_t N, int64_t K, int *plan)
+{
+    if (M <= 0 || N <= 0 || K <= 0 || plan == nullptr) return SQ_ERR_INVALID_ARG;
+    const LinearPlan p = plan_linear(M, N, cdiv(fp4::code_row_bytes(K), 128));
+    plan[0] = p.pairs ? 1 : 0;
+    plan[1] = p.bn;
+    plan[2] = p.pairs ? 2 : p.swap.cs;
+    return SQ_OK;
+}
+
+sq_status sq_debug_rows_fp4_plan(int values, int fmt, sq_dtype dt, int vec, int64_t rows, int64_t K, int *plan)
+{
+    if (!valid_fmt(fmt) || !valid_dt(dt) || rows <= 0 || K <= 0 || plan == nullptr) return SQ_ERR_INVALID_ARG;
+    const RowsPlan p = plan_rows(dt, vec, rows, values ? K : quant_cols(fmt, K), values ? DEQUANT_PER_SM : QUANT_PER_SM);
+    plan[0] = p.rows;
+    plan[1] = static_cast<int>(std::min<int64_t>(cdiv(p.units, p.grid.y), 1 << 30));
+    return SQ_OK;
+}
+
+sq_status sq_debug_kv_plan(int64_t rows, int64_t H, int64_t D, int *plan)
+{
+    const sq_status r = check_kv(SQ_KV_INT8, SQ_F32, H, D);
+    if (r != SQ_OK) return r;
+    if (rows <= 0 || rows > (int64_t(1) << 31) || plan == nullptr) return SQ_ERR_INVALID_ARG;
+    const WritePlan w = plan_write(rows, H, D);
+    const ReadPlan d = plan_read(rows, H, D);
+    plan[0] = w.steps;
+    plan[1] = w.chunks;
+    plan[2] = d.by_rows ? 1 : 0;
+    plan[3] = d.by_rows ? 0 : 1 << d.part_log2;
+    return SQ_OK;
+}
+
 size_t sq_kv_row_bytes(sq_kv_format fmt, int64_t D)
 {
     return valid_kv(fmt) && D > 0 && D <= kv::MAX_D ? static_cast<size_t>(kv::row_bytes(fmt, static_cast<int>(D))) : 0;
@@ -517,19 +608,17 @@ sq_status sq_kv_cache_write(const void *k, const void *v, sq_dtype dt, int64_t T
     kv::WriteArgs a{k, v, T, k_ld, v_ld, num_slots, slots, static_cast<uint8_t *>(k_cache),
                     static_cast<uint8_t *>(v_cache), k_scale, v_scale, static_cast<int>(H), static_cast<int>(D), ll, 0,
                     inverse63(H)};
-    const int64_t steps = cdiv(T * H, 32 >> ll);                // of a warp, for keys and again for values
-    if (cdiv(2 * steps, kv::WARPS) >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
+    const WritePlan plan = plan_write(T, H, D);
+    const int64_t warps = 2 * cdiv(cdiv(T * H, 32 >> ll), plan.steps), blocks = cdiv(warps, kv::WARPS);
+    if (blocks >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
     const int es = dtype_size(dt);
     a.vec = std::min(vec_bytes(k, (k_ld * es) | (D * es)), vec_bytes(v, (v_ld * es) | (D * es)));
     const cudaStream_t st = as_stream(stream);
-    // several steps a warp once that leaves every SM its 64 warps
-    const bool many = 2 * steps >= static_cast<int64_t>(kv::TOKENS) * 64 * sm_count();
     const cudaError_t e = kv_dispatch(dt, fmt, a.vec, [&](auto d, auto f, auto w) {
         constexpr int DT = decltype(d)::value, FMT = decltype(f)::value, VEC = decltype(w)::value;
-        const int64_t tok = D <= 512 && many ? kv::TOKENS : 1;
-        const dim3 grid(static_cast<unsigned>(cdiv(2 * cdiv(steps, tok), kv::WARPS))), block(kv::WARPS * 32);
-        if (D > 512) return launch_pdl(kv::k_kv_write<DT, FMT, VEC, 2, 1>, grid, block, 0, st, a);
-        if (many) return launch_pdl(kv::k_kv_write<DT, FMT, VEC, 1, kv::TOKENS>, grid, block, 0, st, a);
+        const dim3 grid(static_cast<unsigned>(blocks)), block(kv::WARPS * 32);
+        if (plan.chunks == 2) return launch_pdl(kv::k_kv_write<DT, FMT, VEC, 2, 1>, grid, block, 0, st, a);
+        if (plan.steps > 1) return launch_pdl(kv::k_kv_write<DT, FMT, VEC, 1, kv::TOKENS>, grid, block, 0, st, a);
         return launch_pdl(kv::k_kv_write<DT, FMT, VEC, 1, 1>, grid, block, 0, st, a);
     });
     return e == cudaSuccess ? check_launch() : cuda_fail(e);
@@ -570,21 +659,15 @@ sq_status sq_kv_cache_read(sq_kv_format fmt, const void *k_cache, const void *k_
     const cudaStream_t st = as_stream(stream);
     a.page_inv = inverse63(page_size);
     a.head_inv = inverse63(H);
-    // Rows end to end where a warp a token would leave lanes idle or have one
-    // group of heads in flight: 1 head of 64 414 -> 60 us (45 at the copy rate), 2
-    // of 128 107 -> 58, 5 of 128 59 -> 48; 8 of 128 stay a warp a token (69 us
-    // against 73 for 75 k tokens, 2.7 against 3.4 for 64).
-    const bool by_rows = D <= 512 && ((16 << ll) != D || H % (32 >> ll) != 0 || a.groups < 2);
-    // one warp a token, or more while the heads allow and the SMs are not full
-    while (!by_rows && (2 << a.part_log2) <= a.groups && (total << a.part_log2) < static_cast<int64_t>(KV_READ_WARPS) * sm_count())
-        ++a.part_log2;
-    const int64_t warps = by_rows ? cdiv(total * H, 2 * (32 / a.lanes)) : total << a.part_log2;
+    const ReadPlan plan = plan_read(total, H, D);
+    a.part_log2 = plan.part_log2;
+    const int64_t warps = plan.by_rows ? cdiv(total * H, 2 * (32 / a.lanes)) : total << a.part_log2;
     const int64_t blocks = cdiv(warps, kv::WARPS);
     if (blocks >= (int64_t(1) << 31)) return SQ_ERR_UNSUPPORTED;
     const cudaError_t e = kv_dispatch(out_dt, fmt, a.vec, [&](auto d, auto f, auto w) {
         constexpr int DT = decltype(d)::value, FMT = decltype(f)::value, VEC = decltype(w)::value;
         const dim3 grid(static_cast<unsigned>(blocks)), block(kv::WARPS * 32);
-        if (by_rows) return launch_pdl(kv::k_kv_read_rows<DT, FMT, VEC>, grid, block, 0, st, a);
+        if (plan.by_rows) return launch_pdl(kv::k_kv_read_rows<DT, FMT, VEC>, grid, block, 0, st, a);
         return launch_pdl(kv::k_kv_read<DT, FMT, VEC>, grid, block, 0, st, a);
     });
     return e == cudaSuccess ? check_launch() : cuda_fail(e);
