@@ -116,9 +116,9 @@ sq_status sq_debug_kv_plan(int64_t rows, int64_t H, int64_t D, int *plan);
 
 /* Synchronises `stream`, then returns SQ_ERR_TIMEOUT if any kernel of this
  * library recorded a barrier timeout on the current device since the last
- * check, SQ_ERR_INVALID_ARG if a kernel of the key/value cache met an index
- * outside the cache since then (both records are cleared), SQ_ERR_CUDA if the
- * stream reported an error, else SQ_OK. */
+ * check, else SQ_ERR_INVALID_ARG if a kernel of the key/value cache met an index
+ * outside the cache since then (each check clears both records, reported or
+ * not), SQ_ERR_CUDA if the stream reported an error, else SQ_OK. */
 sq_status sq_sync_status(sq_stream stream);
 
 /* -------------------------------------------------------------------------
@@ -591,7 +591,9 @@ sq_status sq_linear_fp4(const uint8_t *xq4, const uint8_t *x_sf, const uint8_t *
  * All four 16-byte aligned.  D <= 1024 and H <= 65536, else SQ_ERR_UNSUPPORTED.
  *
  * Indices are checked on the device: a slot or page outside the cache is not
- * accessed, and sq_sync_status then returns SQ_ERR_INVALID_ARG (once).
+ * accessed, and sq_sync_status then returns SQ_ERR_INVALID_ARG (once; where a
+ * barrier timed out since the last check as well, it returns SQ_ERR_TIMEOUT
+ * alone and clears both).
  * ------------------------------------------------------------------------- */
 typedef enum { SQ_KV_INT8 = 0, SQ_KV_FP8 = 1, SQ_KV_MXFP4 = 2 } sq_kv_format;
 

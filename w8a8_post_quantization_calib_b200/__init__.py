@@ -204,8 +204,8 @@ def set_wait_timeout_ns(ns: int) -> None:
 
 
 def sync_status(stream=None) -> int:
-    """Synchronise the stream; returns the status (0 = OK, 5 = a barrier wait timed out, 1 = a key/value call met an index
-    outside the cache)."""
+    """Synchronise the stream; returns the status (0 = OK, 5 = a barrier wait timed out, else 1 = a key/value call met an
+    index outside the cache; both records are cleared)."""
     return int(_lib.sq_sync_status(_stream(stream)))
 
 
