@@ -357,3 +357,28 @@ def test_no_pages(fmt):
         sq.kv_cache_read(fmt, *cache, dev(table), cu * 0, ko, vo)          # no rows at all
         _sync()
         assert torch.all(ko == 7.0)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("H,D", [(8, 128), (5, 80)])
+def test_rows_before_the_output(fmt, H, D):
+    """A first row before row 0: the sequence's first positions have no row; positions far outside the table read as zeros."""
+    S, T = 4, 24
+    x = rand_x(12, (T, H, D), F16)
+    cache = _cache(T // S, S, H, D, fmt)
+    sq.kv_cache_write(dev(x, F16), dev(x, F16), dev(np.arange(T)), fmt, *cache)
+    val = _oracle_rows(x, fmt, F16)[2]
+    table = dev(np.arange(T // S, dtype=np.int32)[None].repeat(2, 0))
+
+    def read(cu, starts):
+        ko, vo = (torch.full((9, H, D), 7.0, device="cuda") for _ in "kv")
+        sq.kv_cache_read(fmt, *cache, table, dev(np.array(cu, np.int32)), ko, vo, starts=dev(np.array(starts, np.int32)))
+        assert torch.equal(ko, vo)
+        return host(ko)
+
+    o = read([-5, 3, 8], [2, 1])
+    _sync()
+    assert np.array_equal(o[:3], val[7:10]) and np.array_equal(o[3:8], val[1:6]) and np.all(o[8] == 7.0)
+    o = read([-2 ** 31, 2, 6], [2 ** 31 - 1, 2 ** 31 - 1])            # positions around 2^32, and around 2^31
+    assert sq.sync_status() == 1
+    assert np.all(o[:6] == 0) and np.all(o[6:] == 7.0)

@@ -184,6 +184,16 @@ __device__ __forceinline__ int sequence_of(const int32_t *cu, int B, int64_t t, 
     return lo < B ? lo : -1;
 }
 
+// The page that holds position `pos` of sequence b (-1: outside the table), and
+// its column pi.  Output rows and starts are below 2^31, so positions are below
+// 2^32 (with a first row below 0 they can be higher: outside); page_size < 2^31,
+// so the quotient's error, pos / 2^63, is below 1 / page_size.
+__device__ __forceinline__ int64_t page_of(const ReadArgs &a, int b, int64_t pos, int64_t &pi)
+{
+    pi = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(pos) << 1, a.page_inv));
+    return (static_cast<uint64_t>(pos) >> 32) == 0 && pi < a.max_pages ? __ldg(a.table + b * a.max_pages + pi) : -1;
+}
+
 // 16 codes of a row and their scale
 template <int FMT>
 __device__ __forceinline__ void load_codes(const uint8_t *cache, const void *scale, int64_t row, int rb, int sb, int c,
@@ -250,9 +260,8 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv_read(const ReadArgs a)
     const int b = t < a.total ? sequence_of(a.cu, a.B, t, lane) : -1;
     if (b >= 0) {
         const int64_t pos = t - __ldg(a.cu + b) + (a.starts != nullptr ? __ldg(a.starts + b) : 0);
-        // 0 <= pos < 2^32 and page_size < 2^31: the error of the quotient, pos / 2^63, is below 1 / page_size
-        const int64_t pi = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(pos) << 1, a.page_inv));
-        const int64_t page = pos >= 0 && pi < a.max_pages ? __ldg(a.table + b * a.max_pages + pi) : -1;
+        int64_t pi;
+        const int64_t page = page_of(a, b, pos, pi);
         const bool ok = page >= 0 && page < a.num_pages;
         if (!ok && lane == 0) bad_index();
         const int64_t row0 = (page * a.page_size + (pos - pi * a.page_size)) * a.H, out0 = t * a.H;
@@ -330,8 +339,8 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv_read_rows(const ReadArgs a)
             }
             if (t < first || t >= end) continue;
             const int64_t pos = t - first + start;
-            const int64_t pi = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(pos) << 1, a.page_inv));
-            const int64_t page = pos >= 0 && pi < a.max_pages ? __ldg(a.table + b * a.max_pages + pi) : -1;
+            int64_t pi;
+            const int64_t page = page_of(a, b, pos, pi);
             if (page >= 0 && page < a.num_pages) {
                 row[u] = (page * a.page_size + (pos - pi * a.page_size)) * a.H + (r - t * a.H);
             } else {
