@@ -13,13 +13,17 @@
 // ceil(D / 32)), the padding holding zero codes, so that every row starts on
 // 16 bytes; scales fp32 [slots][H], MXFP4 bytes [slots][H][ceil(D / 32)].
 //
-// Both kernels move bytes: a lane owns 16 elements (a 32-byte access of a
-// 16-bit type), a power of two of lanes a row, so that a row's maximum is a
-// few shuffles and a warp covers 32 / lanes heads of one token.  8 heads of 128
-// bf16: 10.3 k tokens written as E4M3 in 13.3 us (64 MB, 4.8 TB/s) and read
-// back in 13.3; contexts of 75 k tokens read back from MXFP4 in 69.8 us (400
-// MB, 5.7 TB/s of 6.57 copied), from INT8 in 87.  A decode step's 64 tokens
-// take 1.6 and 2.6 us: launches and chains of loads.
+// The three kernels move bytes: a lane owns 16 elements (a 32-byte access of a
+// 16-bit type).
+//   k_kv_write      rows of all tokens end to end, a power of two of lanes a
+//                   row, so that a row's maximum is a few shuffles (heads of 80
+//                   or 96 leave lanes idle)
+//   k_kv_read       a warp, or several, a token; the same lanes a row
+//   k_kv_read_rows  rows end to end, ceil(D / 16) lanes a row
+// 8 heads of 128 bf16: 10.3 k tokens written as E4M3 in 13.3 us (64 MB, 4.8
+// TB/s) and read back in 13.1; contexts of 75 k tokens read back from MXFP4 in
+// 69.2 us (400 MB, 5.8 TB/s of 6.57 copied), from INT8 in 87.  A decode step's
+// 64 tokens take 1.7 and 2.7 us: launches and chains of loads.
 #pragma once
 
 #include "common.cuh"

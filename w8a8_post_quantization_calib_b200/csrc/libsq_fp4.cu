@@ -39,8 +39,9 @@ inline int vec_bytes(const void *p, int64_t ld_bytes)
     return (a & 31) == 0 ? 32 : (a & 15) == 0 ? 16 : (a & 7) == 0 ? 8 : (a & 3) == 0 ? 4 : 0;
 }
 
-// two blocks of the quantiser fit an SM (one pass over the SMs), about two of
-// the dequantiser: measured best of 2, 3, 4, 6, 8
+// Blocks an SM that share a strip's rows, measured best of 2, 3, 4, 6, 8.  Two
+// fit at once of either kernel for 16-bit types and four rows a thread (124 and
+// 93 registers): one pass over the SMs for the quantiser, two for the dequantiser.
 constexpr int QUANT_PER_SM = 2, DEQUANT_PER_SM = 4;
 
 // Column strips of 512 x units of rows, at most `per_sm` blocks a SM.
