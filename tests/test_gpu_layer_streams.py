@@ -158,3 +158,49 @@ def test_a_stream_under_capture():
     other.write(k, k, slots)
     assert sq.sync_status() == 0
     assert torch.equal(cache.k, other.k) and torch.equal(cache.v_scale, other.v_scale)
+
+
+@pytest.mark.parametrize("kind", MAKE)
+def test_a_stream_forked_inside_a_capture(kind):
+    """Calls on a second stream while the current one captures: both end up in the graph."""
+    k = _k(kind)
+    w, x = _inputs(k)
+    c = layer.Calibrator(k)
+    c.add_batch(x)
+    lin = MAKE[kind](w, c.act_max)
+    a, b = x[:M].clone(), x[M:2 * M].clone()
+    st, side, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    lin.forward(a)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=st):
+        ya, yb = lin.forward(a), lin.forward(b, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for seed in (7, 8):
+        fresh = dev(rand_x(seed, (2 * M, k), BF16, 1.5), BF16)
+        a.copy_(fresh[:M])
+        b.copy_(fresh[M:])
+        graph.replay()
+        assert torch.equal(ya, lin.forward(a)) and torch.equal(yb, lin.forward(b))
+    assert sq.sync_status() == 0
+
+
+@pytest.mark.parametrize("kind", MAKE)
+def test_the_default_stream_from_another_one(kind):
+    k = _k(kind)
+    w, x = _inputs(k)
+    c = layer.Calibrator(k)
+    c.add_batch(x)
+    lin = MAKE[kind](w, c.act_max)
+    want = lin.forward(x)
+    torch.cuda.synchronize()
+    for stream in (0, torch.cuda.default_stream()):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            torch.cuda._sleep(SLEEP)
+            x2 = x.clone()
+            y = lin.forward(x2, stream=stream)
+            del x2
+            spoilt = _spoil(2 * x.numel())
+        torch.cuda.synchronize()
+        assert sq.sync_status() == 0
+        assert torch.equal(y, want)
+        del spoilt
