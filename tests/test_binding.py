@@ -59,6 +59,18 @@ else:
     assert r.returncode == 0, r.stderr
 
 
+def test_a_prerelease_of_torch_has_its_release_number(tmp_path):
+    d = _package_without_binding(tmp_path)
+    (d / "_sqbind.py").write_text("TORCH_VERSION = '9.8.7'\ndef set_error(e): pass\ndef dequant_fp4(*a): pass\n")
+    r = _run(tmp_path, f"""
+import torch
+import {PKG} as sq
+torch.__version__ = "9.8.7a0+git1234567"
+sq.dequant_fp4(None, None, sq.MXFP4, None)
+""")
+    assert r.returncode == 0, r.stderr
+
+
 def test_the_binding_in_the_tree_loads():
     torch = pytest.importorskip("torch")
     sq = pytest.importorskip(PKG)

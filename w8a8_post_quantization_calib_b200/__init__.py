@@ -30,6 +30,7 @@ from __future__ import annotations
 import ctypes
 import importlib
 import os
+import re
 
 import torch
 
@@ -150,7 +151,7 @@ class _Binding:
             module = importlib.import_module(__name__ + "._sqbind")            # links libsq.so, loaded above
         except ImportError as e:
             raise ImportError(f"{_HERE}/_sqbind.so is missing or does not fit this Python and torch ({e}): {hint}") from e
-        if module.TORCH_VERSION != torch.__version__.split("+")[0]:
+        if module.TORCH_VERSION != re.match(r"[0-9.]*", torch.__version__)[0]:          # "2.11.0a0+git1" is 2.11.0
             raise ImportError(f"{_HERE}/_sqbind.so was built for torch {module.TORCH_VERSION}, not {torch.__version__}: {hint}")
         module.set_error(SQError)
         _bind = module
