@@ -204,3 +204,27 @@ def test_the_default_stream_from_another_one(kind):
         assert sq.sync_status() == 0
         assert torch.equal(y, want)
         del spoilt
+
+
+@pytest.mark.parametrize("kind", MAKE)
+def test_refusals_leave_the_current_stream(kind):
+    """A tensor that is not on a GPU is refused as without stream=, and the caller's stream is the current one again."""
+    k = _k(kind)
+    w, x = _inputs(k)
+    c = layer.Calibrator(k)
+    c.add_batch(x)
+    lin = MAKE[kind](w, c.act_max)
+    st, cur = torch.cuda.Stream(), torch.cuda.current_stream()
+    calls = [lambda: lin.forward(x.cpu(), stream=st), lambda: lin.forward(x[:, :k - 8], stream=st),
+             lambda: MAKE[kind](w.cpu(), c.act_max, stream=st), lambda: c.add_batch(x.cpu(), stream=st)]
+    for call in calls:
+        with pytest.raises((TypeError, ValueError, sq.SQError)):
+            call()
+        assert torch.cuda.current_stream() == cur
+    cache = layer.PagedKVCache(2, 4, 2, 64)
+    kv = torch.zeros(3, 2, 64, device="cuda")
+    with pytest.raises(TypeError):
+        cache.write(kv, kv, torch.arange(3), stream=st)
+    with pytest.raises(TypeError):
+        cache.write(kv, kv, None, stream=st)
+    assert torch.cuda.current_stream() == cur and sq.sync_status() == 0

@@ -50,12 +50,16 @@ class _Side(_Here):
     def __enter__(self):
         graph = torch.cuda.is_current_stream_capturing()
         self.context.__enter__()
-        # a graph under capture does not wait for work outside it: that is done, or not, when it is replayed
-        if graph or not torch.cuda.is_current_stream_capturing():
-            self.side.wait_stream(self.caller)
-        for t in self.tensors:
-            if t is not None:
-                t.record_stream(self.side)
+        try:
+            # a graph under capture does not wait for work outside it: that is done, or not, when it is replayed
+            if graph or not torch.cuda.is_current_stream_capturing():
+                self.side.wait_stream(self.caller)
+            for t in self.tensors:
+                if isinstance(t, torch.Tensor) and t.is_cuda:          # others are refused by the call
+                    t.record_stream(self.side)
+        except BaseException:
+            self.context.__exit__(None, None, None)
+            raise
         return self
 
     def __exit__(self, *exc):
