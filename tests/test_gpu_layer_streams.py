@@ -228,3 +228,18 @@ def test_refusals_leave_the_current_stream(kind):
     with pytest.raises(TypeError):
         cache.write(kv, kv, None, stream=st)
     assert torch.cuda.current_stream() == cur and sq.sync_status() == 0
+
+
+def test_a_stream_of_another_device_is_refused():
+    """Not made the current one: the kernels would run on its device, which cannot reach the tensors."""
+    class Other(torch.cuda.Stream):
+        device = torch.device("cuda", 1)
+
+    w, x = _inputs(K)
+    c = layer.Calibrator(K)
+    c.add_batch(x)
+    lin = MAKE["mxfp4"](w, c.act_max)
+    for call in (lambda: lin.forward(x, stream=Other()), lambda: c.add_batch(x, stream=Other())):
+        with pytest.raises(ValueError, match="cuda:1"):
+            call()
+    assert sq.sync_status() == 0

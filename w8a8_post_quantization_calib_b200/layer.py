@@ -79,6 +79,8 @@ def _on(stream, *tensors):
     if stream is None:
         return _HERE
     caller = torch.cuda.current_stream()
+    if isinstance(stream, torch.cuda.Stream) and stream.device != caller.device:
+        raise ValueError(f"the stream is on {stream.device}, the current device is {caller.device}")
     address = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if address == caller.cuda_stream:
         return _HERE
