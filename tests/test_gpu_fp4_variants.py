@@ -127,6 +127,27 @@ def test_withheld_stage_of_a_pair_times_out_and_context_survives(M, N, K, bn, fm
     _product(M, N, K, fmt, BF16, False)
 
 
+@pytest.mark.parametrize("bn,cs", [v for v in cases.LINEAR_SWAP if v[1] > 1])
+def test_withheld_stage_of_a_cluster_times_out_and_context_survives(bn, cs):
+    """The CTA without its stage and those that wait for its partial sums give up; the next product is right."""
+    M, N, K = cases.LINEAR_SWAP[bn, cs][0]
+    assert linear(M, N, K) == (0, bn, cs)
+    q, sf = _buffers(M, K, NV, 0)
+    wq, wsf = _buffers(N, K, NV, 0)
+    y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    _sync()
+    sq.set_wait_timeout_ns(20_000_000)
+    sq.lib().sq_debug_inject(1)
+    try:
+        sq.linear_fp4(q, sf, wq, wsf, NV, y)
+        assert sq.sync_status() == 5
+        assert sq.sync_status() == 0
+    finally:
+        sq.lib().sq_debug_inject(0)
+        sq.set_wait_timeout_ns(0)
+    _product(M, N, K, NV, BF16, False)
+
+
 @pytest.mark.parametrize("bn", cases.LINEAR_PAIRS)
 def test_linear_pairs_in_a_graph_and_on_two_streams(bn):
     """Replayed, and side by side on two streams: the bits of a call alone."""

@@ -462,6 +462,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 2)
     if constexpr (CS > 1) ptx::cluster_meet();   // no CTA leaves while another may still write to its stages
     pdl_trigger();                     // every output of this CTA is written
     if (warp == 1) {
+        // A CTA that gave up may have been sent partial sums that it did not
+        // wait for: issued before the meeting, but asynchronous.  It stays
+        // until they have landed (a store within the cluster takes ~1 us).
+        if (CS > 1 && *abort_flag != 0) {
+            for (int i = 0; i < 50; ++i) __nanosleep(1000);
+        }
         __syncwarp();
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem_base, C::TMEM_COLS);
